@@ -422,6 +422,121 @@ zb_status zb_gather_rows(const uint16_t* X, int32_t heads, int64_t n_in, int64_t
                          const int32_t* rows, uint16_t* out, void* stream);
 
 /*
+ * Rotary positions.  The rotated part of a head is `axes` equal runs of
+ * features (one for sequence positions, two for the row and column of a
+ * patch), each with n = rotary_dim / (2 axes) pairs; pair i of axis a turns by
+ * theta = pos[a][token] * f_i:
+ *   (x1, x2) -> magnitude * (x1 cos - x2 sin, x2 cos + x1 sin).
+ * Pairs are features (i, i + n) of the run (ZB_ROPE_HALF) or (2i, 2i + 1)
+ * (ZB_ROPE_INTERLEAVED).  Features past rotary_dim pass unchanged.  The
+ * gradient of the rotation is the rotation by the opposite angles.
+ *
+ * zb_rope_frequencies writes, on the HOST, the frequencies as turns a position
+ * in 64-bit fixed point (turns[i] = f_i / 2 pi * 2^64; what zb_rotation wants
+ * on the device), so that angles of far positions lose nothing:
+ *   ZB_ROPE_PLAIN   f_i = base^(-i / n)
+ *   ZB_ROPE_LINEAR  f_i / factor
+ *   ZB_ROPE_NTK     base * factor^(n / (n - 1)) in the place of base
+ *   ZB_ROPE_PARTS   by the rotations R_i = original_len * f_i / 2 pi of a pair
+ *                   over the trained length: f_i / factor for R_i <= low, f_i
+ *                   for R_i >= high, their mix linear in R_i between; magnitude
+ *                   0.1 ln(factor) + 1 ("YaRN: Efficient Context Window
+ *                   Extension of Large Language Models", NTK-by-parts)
+ *   out: turns int64 [pairs] HOST, radians fp64 [pairs] HOST or NULL (f_i),
+ *        magnitude HOST or NULL (1 but for ZB_ROPE_PARTS)
+ * Errors: ZB_ERR_SHAPE (pairs not in 1..32, base <= 1, factor < 1, a length
+ * <= 0, low >= high, ZB_ROPE_NTK with one pair), ZB_ERR_NULL,
+ * ZB_ERR_UNSUPPORTED (unknown scaling).
+ */
+enum { ZB_ROPE_HALF = 0, ZB_ROPE_INTERLEAVED = 1 };
+enum { ZB_ROPE_PLAIN = 0, ZB_ROPE_LINEAR = 1, ZB_ROPE_NTK = 2, ZB_ROPE_PARTS = 3 };
+
+zb_status zb_rope_frequencies(int32_t pairs, double base, int32_t scaling, double factor, double original_len,
+                              double low, double high, int64_t* turns, double* radians, float* magnitude);
+
+/* Where the rows of a bf16 [batch][heads][n_tokens][64] tensor lie: strides in
+ * elements, multiples of 8 and not negative; a row's 64 features are contiguous. */
+typedef struct zb_rows {
+    int64_t batch_stride, head_stride, token_stride;
+} zb_rows;
+
+typedef struct zb_rotation {
+    const int32_t* pos;       /* DEVICE int32 [batch][axes][n_tokens]                     */
+    int64_t pos_batch_stride; /* elements between two sequences' positions; 0: shared     */
+    const int64_t* turns;     /* DEVICE int64 [rotary_dim / (2 axes)]                     */
+    int32_t rotary_dim;       /* 0 (no rotation) .. 64, a multiple of 16 * axes           */
+    int32_t axes;             /* 1 or 2                                                   */
+    int32_t layout;           /* ZB_ROPE_HALF or ZB_ROPE_INTERLEAVED                      */
+    float magnitude;          /* > 0, normally 1                                          */
+    int32_t inverse;          /* zb_rope: nonzero turns by the opposite angles            */
+} zb_rotation;
+
+/*
+ * Y = X rotated (see above); fp32 arithmetic, rounded to bf16 once.  With
+ * rot.inverse, X the gradient of a forward call's Y gives the gradient of its X.
+ *   in : X bf16, rows at x_rows (strides of 0 repeat rows)
+ *   out: Y bf16, rows at y_rows (no two of them may overlap).  Y may be X
+ *        itself, with the same strides.
+ * Errors: ZB_ERR_SHAPE (also output rows that overlap), ZB_ERR_UNSUPPORTED
+ * (head_dim, axes, layout, rotary_dim not a multiple of 16 * axes, more than
+ * 2^31 - 1 tokens), ZB_ERR_ALIGN (also strides that are negative or not
+ * multiples of 8), ZB_ERR_NULL, ZB_ERR_CUDA.
+ */
+zb_status zb_rope(const uint16_t* X, zb_rows x_rows, int32_t batch, int32_t heads, int64_t n_tokens,
+                  int32_t head_dim, zb_rotation rot, uint16_t* Y, zb_rows y_rows, void* stream);
+
+/* The norm over each head's 64 features that comes before the rotation. */
+enum { ZB_NORM_NONE = 0, ZB_NORM_RMS = 1, ZB_NORM_LAYER = 2 };
+typedef struct zb_qk_norm {
+    int32_t kind;         /* ZB_NORM_*                                                    */
+    float eps;            /* >= 0, added to the mean of squares                           */
+    const float *wq, *wk; /* DEVICE fp32 [64] weights of queries and keys; NULL: ones     */
+    const float *bq, *bk; /* DEVICE fp32 [64] biases, ZB_NORM_LAYER alone; NULL: zeros    */
+} zb_qk_norm;
+
+/*
+ * Queries and keys of a layer made ready for its attention in one pass:
+ * y = w * (x - m) / sqrt(mean((x - m)^2) + eps) + b with m = 0 (ZB_NORM_RMS) or
+ * the row's mean (ZB_NORM_LAYER), then the rotation; fp32 arithmetic, rounded to
+ * bf16 once.  ZB_NORM_NONE ignores w and b and only rotates; rotary_dim 0 only
+ * normalises.
+ *   in : Q bf16, heads_q heads at q_rows; K bf16, heads_k heads at k_rows
+ *        (heads_k 0: no keys, K and Ko are not looked at), e.g. both inside the
+ *        output [batch][token][head][64] of one projection
+ *   out: Qo, Ko bf16 [batch][heads][n_tokens][64] contiguous, not overlapping
+ *        the inputs
+ * Errors: as zb_rope; ZB_ERR_SHAPE for eps < 0; ZB_ERR_UNSUPPORTED for an unknown
+ * kind, a bias without ZB_NORM_LAYER and rot.inverse.
+ */
+zb_status zb_qk_norm_rope(const uint16_t* Q, zb_rows q_rows, int32_t heads_q, const uint16_t* K, zb_rows k_rows,
+                          int32_t heads_k, int32_t batch, int64_t n_tokens, int32_t head_dim, zb_qk_norm norm,
+                          zb_rotation rot, uint16_t* Qo, uint16_t* Ko, void* stream);
+
+/*
+ * Gradient of zb_qk_norm_rope: with dy the gradient turned back, xh the
+ * normalised row, g = w dy and r = 1 / sqrt(mean square + eps),
+ *   dx = r (g - xh mean(g xh))  less r mean(g) for ZB_NORM_LAYER,
+ *   dw = sum over all rows of dy xh,  db = sum over all rows of dy.
+ * The row's statistics are computed again from Q and K: the forward call keeps
+ * nothing.  Sums run in fp32 per CTA and fp64 across CTAs in a fixed order (the
+ * result does not depend on scheduling).
+ *   in : dQo, dKo bf16 contiguous; Q, K and norm, rot as in the forward call
+ *   out: dQ, dK bf16, rows at dq_rows, dk_rows (no overlap; e.g. inside one
+ *        projection's gradient; not the inputs' memory); dwq, dwk, dbq, dbk
+ *        fp32 [64], each may be NULL (dw without a norm, db without
+ *        ZB_NORM_LAYER must be: ZB_ERR_UNSUPPORTED)
+ *   ws : zb_qk_norm_rope_backward_workspace_bytes() bytes, 16-byte aligned,
+ *        owned by the caller and not shared with a call running at the same time
+ * One launch, two with a dw or db.  Errors: as zb_qk_norm_rope, ZB_ERR_WORKSPACE.
+ */
+size_t zb_qk_norm_rope_backward_workspace_bytes(void);
+zb_status zb_qk_norm_rope_backward(const uint16_t* dQo, const uint16_t* dKo, const uint16_t* Q, zb_rows q_rows,
+                                   int32_t heads_q, const uint16_t* K, zb_rows k_rows, int32_t heads_k, int32_t batch,
+                                   int64_t n_tokens, int32_t head_dim, zb_qk_norm norm, zb_rotation rot, uint16_t* dQ,
+                                   zb_rows dq_rows, uint16_t* dK, zb_rows dk_rows, float* dwq, float* dwk, float* dbq,
+                                   float* dbk, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then report and clear the current device's status
  * word: ZB_OK, or the first of ZB_ERR_TIMEOUT / ZB_ERR_INDEX / ZB_ERR_SINGULAR
  * recorded by a kernel since the last call.  ZB_ERR_CUDA if the stream or the

@@ -43,6 +43,7 @@ LAUNCHES_PER_CALL = {
     "zb_linear_state": 2, "zb_linear_apply": 1, "zb_linear_attn": 3, "zb_affine_fit": 3, "zb_gather_tiles": 1,
     "zb_key_mean": 2, "zb_linear_state_centered": 2, "zb_block_mass": 1, "zb_block_mass_top_fraction": 1,
     "zb_block_mass_selected_fraction": 1, "zb_gather_rows": 1, "zb_spatial_order": 0,
+    "zb_rope": 1, "zb_qk_norm_rope": 1, "zb_qk_norm_rope_backward": 2,
 }
 
 
@@ -87,6 +88,17 @@ def _check(status: int, what: str) -> None:
 
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+def _call(device: torch.device, name: str, *args) -> None:
+    """Call a library function on `device`'s current stream (the last argument), whichever device is current."""
+    fn = getattr(_lib_handle(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    _check(st, name)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -635,3 +647,10 @@ class HybridLayer:
     def dense_launches(self) -> int:
         """Kernels of the calibration's dense pass (the dense kernel, and the merge when split)."""
         return LAUNCHES_PER_CALL["zb_dense_attn_split" if self.calib_splits > 1 else "zb_dense_attn"]
+
+
+from .positions import (RopeFrequencies, grid_positions, zb_qk_norm_rope, zb_qk_norm_rope_backward,  # noqa: E402
+                        zb_rope, zb_rope_frequencies)
+
+__all__ += ["RopeFrequencies", "grid_positions", "zb_rope", "zb_rope_frequencies", "zb_qk_norm_rope",
+            "zb_qk_norm_rope_backward"]

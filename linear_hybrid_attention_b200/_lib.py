@@ -8,10 +8,24 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libzb.so")
 
 c_i32, c_i64, c_f32, c_sz, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+c_f64 = ctypes.c_double
 
 
 class ZbShape(ctypes.Structure):
     _fields_ = [("heads", c_i32), ("n_tokens", c_i64), ("head_dim", c_i32), ("tile", c_i32)]
+
+
+class ZbRows(ctypes.Structure):
+    _fields_ = [("batch_stride", c_i64), ("head_stride", c_i64), ("token_stride", c_i64)]
+
+
+class ZbRotation(ctypes.Structure):
+    _fields_ = [("pos", c_vp), ("pos_batch_stride", c_i64), ("turns", c_vp), ("rotary_dim", c_i32), ("axes", c_i32),
+                ("layout", c_i32), ("magnitude", c_f32), ("inverse", c_i32)]
+
+
+class ZbQkNorm(ctypes.Structure):
+    _fields_ = [("kind", c_i32), ("eps", c_f32), ("wq", c_vp), ("wk", c_vp), ("bq", c_vp), ("bk", c_vp)]
 
 
 STATUS = {
@@ -52,6 +66,14 @@ PROTOTYPES = {
     "zb_affine_fit_workspace_bytes": (c_sz, [c_i32, c_i64, c_i32]),
     "zb_affine_fit": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "zb_gather_tiles": (c_i32, [c_vp, ZbShape, c_vp, c_i32, c_vp, c_vp]),
+    "zb_rope_frequencies": (c_i32, [c_i32, c_f64, c_i32, c_f64, c_f64, c_f64, c_f64, c_vp, c_vp, c_vp]),
+    "zb_rope": (c_i32, [c_vp, ZbRows, c_i32, c_i32, c_i64, c_i32, ZbRotation, c_vp, ZbRows, c_vp]),
+    "zb_qk_norm_rope": (c_i32, [c_vp, ZbRows, c_i32, c_vp, ZbRows, c_i32, c_i32, c_i64, c_i32, ZbQkNorm, ZbRotation,
+                                c_vp, c_vp, c_vp]),
+    "zb_qk_norm_rope_backward_workspace_bytes": (c_sz, []),
+    "zb_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_vp, ZbRows, c_i32, c_vp, ZbRows, c_i32, c_i32, c_i64, c_i32,
+                                         ZbQkNorm, ZbRotation, c_vp, ZbRows, c_vp, ZbRows, c_vp, c_vp, c_vp, c_vp,
+                                         c_vp, c_sz, c_vp]),
     "zb_last_device_status": (c_i32, [c_vp]),
 }
 
