@@ -537,6 +537,112 @@ zb_status zb_qk_norm_rope_backward(const uint16_t* dQo, const uint16_t* dKo, con
                                    float* dbk, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * 8-bit key/value cache.  A head (batch folded in) owns `slots` blocks of
+ * `block` tokens.  The codes of a block share one scale for its keys and one for
+ * its values: scale = max|x| / M in fp32 (M = 127 for ZB_KV8_INT8, 448 for
+ * ZB_KV8_E4M3), code = the nearest to x / scale, of two as near the even one.  A
+ * block with a value that is not finite has the scale NaN and reads as NaN.
+ * Logical block b of head h lies in slot table[h][b]; `table` starts as any
+ * order of 0..slots-1 for each head, and zb_kv8_evict reorders it.
+ *   k, v             [heads][slots][block][64] codes
+ *   k_scale, v_scale fp32 [heads][slots]
+ *   k_tail, v_tail   bf16 [heads][block][64]: the original rows of the block in
+ *                    progress (zb_kv8_append alone uses them)
+ *   table            int32 [heads][slots]
+ *   mass             fp32 [heads][slots] or NULL: attention weight each slot's
+ *                    block has received
+ * The lengths are a separate DEVICE array int32 [heads].  A length out of
+ * [0, slots * block] is cut to it; a table entry out of range is read as slot 0
+ * and sets ZB_ERR_INDEX in the device status.
+ */
+enum { ZB_KV8_INT8 = 0, ZB_KV8_E4M3 = 1 };
+
+typedef struct zb_kv8 {
+    int32_t heads;    /* 1..65535                                                 */
+    int32_t slots;    /* >= 1, slots * block < 2^31                               */
+    int32_t head_dim; /* must be 64                                               */
+    int32_t block;    /* 16, 32, 64 or 128                                        */
+    int32_t format;   /* ZB_KV8_INT8 or ZB_KV8_E4M3                               */
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    uint16_t *k_tail, *v_tail;
+    int32_t* table;
+    float* mass;
+} zb_kv8;
+
+/*
+ * Append n_new tokens to every head's cache, after its first lens[h] tokens.
+ * The block in progress is quantised again from its original rows, so the
+ * cache's contents do not depend on how tokens are split over calls.  Codes of a
+ * block behind its last token are zeros; blocks that the call opens get mass 0.
+ *   in : K, V bf16 [heads][n_new][64];  lens int32 [heads]
+ *   out: the cache;  lens_out int32 [heads] = lens + n_new.  lens_out may be
+ *        lens itself (a second launch where n_new spans several units of 128
+ *        tokens) or an array of its own.
+ * A head whose new length would pass slots * block is left as it is, keeps its
+ * length and sets ZB_ERR_INDEX in the device status.
+ * Errors: ZB_ERR_SHAPE (n_new < 1 or above slots * block), ZB_ERR_UNSUPPORTED
+ * (head_dim, block, format, heads, size), ZB_ERR_NULL, ZB_ERR_ALIGN, ZB_ERR_CUDA.
+ */
+zb_status zb_kv8_append(zb_kv8 cache, const uint16_t* K, const uint16_t* V, int64_t n_new, const int32_t* lens,
+                        int32_t* lens_out, void* stream);
+
+/*
+ * The newest n tokens of every head as bf16 (code * scale in fp32, rounded
+ * once), in the layout the bf16 attention calls take: row i is token
+ * lens[h] - n + i, zeros where that is before the first token.
+ *   out: K, V bf16 [heads][n][64]
+ * Errors: as zb_kv8_append.
+ */
+zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K, uint16_t* V, void* stream);
+
+/*
+ * Softmax attention of new queries over the cache: the heads_q / heads query
+ * heads h * heads_q / heads ... of each cache head h attend to its first lens[h]
+ * tokens, all of them (causal == 0), or, with the n_q queries as the newest of
+ * those tokens, query i to tokens 0 .. lens[h] - n_q + i (causal != 0).  A query
+ * that sees no token gets zeros and an lse of -inf.
+ *   in : Q bf16 [heads_q][n_q][64], heads_q a multiple of cache.heads;  lens
+ *   out: O bf16 [heads_q][n_q][64];  lse fp32 [heads_q][n_q] natural-log
+ *        log-sum-exp of each row's logits (may be NULL);  with add_mass, each
+ *        block's softmax weight, summed over its tokens and the rows of its
+ *        head's queries, is added to cache.mass (must not be NULL)
+ *   ws : zb_kv8_attn_workspace_bytes() bytes, 16-byte aligned, owned by the
+ *        caller and not shared with a call running at the same time
+ * fp16 tensor-core products of exact codes, fp32 logits, sums and outputs, O
+ * rounded to bf16 once.  The result does not depend on scheduling.
+ * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0), ZB_ERR_NULL,
+ * ZB_ERR_ALIGN, ZB_ERR_UNSUPPORTED (also more than 2^31 - 1 query rows of a cache
+ * head), ZB_ERR_WORKSPACE, ZB_ERR_CUDA; ZB_ERR_TIMEOUT in the device status if a
+ * bounded wait gave up.
+ */
+size_t zb_kv8_attn_workspace_bytes(zb_kv8 cache, int32_t heads_q, int64_t n_q, int32_t add_mass);
+zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q, zb_kv8 cache, const int32_t* lens,
+                      int32_t causal, float scale, uint16_t* O, float* lse, int32_t add_mass, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Eviction by accumulated attention weight: every head keeps at most `budget`
+ * blocks.  Its first `sinks` and last `recent` blocks (the one in progress among
+ * them) stay; of the others those with the largest mass[h][table[h][b]], equal
+ * ones by the lower b, fill the budget.  Kept blocks move up in order, the freed
+ * slots follow them in order, entries of unused slots stay: no code is moved,
+ * and scales, tails and weights go with their slots.  A head within the budget
+ * keeps everything.  A weight that is NaN counts as the largest if its sign is
+ * clear, else as the smallest.
+ *   in : table, mass, lens as in zb_kv8;  1 <= sinks + recent <= budget <= slots
+ *        (sinks >= 0, recent >= 1)
+ *   out: table_out int32 [heads][slots], not table itself;  lens_out int32
+ *        [heads] = lens - block * blocks evicted (may be lens itself);  kept int32
+ *        [heads][budget] or NULL: the kept logical blocks, ascending, then -1
+ * Errors: ZB_ERR_SHAPE, ZB_ERR_UNSUPPORTED (block, heads, size), ZB_ERR_NULL,
+ * ZB_ERR_ALIGN, ZB_ERR_CUDA.
+ */
+zb_status zb_kv8_evict(const int32_t* table, const float* mass, const int32_t* lens, int32_t heads, int32_t slots,
+                       int32_t block, int32_t budget, int32_t sinks, int32_t recent, int32_t* table_out,
+                       int32_t* lens_out, int32_t* kept, void* stream);
+
+/*
  * Synchronise `stream`, then report and clear the current device's status
  * word: ZB_OK, or the first of ZB_ERR_TIMEOUT / ZB_ERR_INDEX / ZB_ERR_SINGULAR
  * recorded by a kernel since the last call.  ZB_ERR_CUDA if the stream or the

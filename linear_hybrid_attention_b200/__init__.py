@@ -44,6 +44,7 @@ LAUNCHES_PER_CALL = {
     "zb_key_mean": 2, "zb_linear_state_centered": 2, "zb_block_mass": 1, "zb_block_mass_top_fraction": 1,
     "zb_block_mass_selected_fraction": 1, "zb_gather_rows": 1, "zb_spatial_order": 0,
     "zb_rope": 1, "zb_qk_norm_rope": 1, "zb_qk_norm_rope_backward": 2,
+    "zb_kv8_append": 1, "zb_kv8_read": 1, "zb_kv8_attn": 2, "zb_kv8_evict": 1,
 }
 
 
@@ -654,3 +655,9 @@ from .positions import (RopeFrequencies, grid_positions, zb_qk_norm_rope, zb_qk_
 
 __all__ += ["RopeFrequencies", "grid_positions", "zb_rope", "zb_rope_frequencies", "zb_qk_norm_rope",
             "zb_qk_norm_rope_backward"]
+
+from .cache import (CachedAttention, KV8Cache, zb_kv8_append, zb_kv8_attn, zb_kv8_attn_workspace_bytes,  # noqa: E402
+                    zb_kv8_evict, zb_kv8_read)
+
+__all__ += ["CachedAttention", "KV8Cache", "zb_kv8_append", "zb_kv8_attn", "zb_kv8_attn_workspace_bytes",
+            "zb_kv8_evict", "zb_kv8_read"]

@@ -28,6 +28,12 @@ class ZbQkNorm(ctypes.Structure):
     _fields_ = [("kind", c_i32), ("eps", c_f32), ("wq", c_vp), ("wk", c_vp), ("bq", c_vp), ("bk", c_vp)]
 
 
+class ZbKv8(ctypes.Structure):
+    _fields_ = [("heads", c_i32), ("slots", c_i32), ("head_dim", c_i32), ("block", c_i32), ("format", c_i32),
+                ("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("k_tail", c_vp), ("v_tail", c_vp),
+                ("table", c_vp), ("mass", c_vp)]
+
+
 STATUS = {
     0: "ZB_OK", 1: "ZB_ERR_NULL", 2: "ZB_ERR_SHAPE", 3: "ZB_ERR_ALIGN", 4: "ZB_ERR_UNSUPPORTED",
     5: "ZB_ERR_WORKSPACE", 6: "ZB_ERR_CUDA", 7: "ZB_ERR_TIMEOUT", 8: "ZB_ERR_DEVICE",
@@ -74,6 +80,11 @@ PROTOTYPES = {
     "zb_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_vp, ZbRows, c_i32, c_vp, ZbRows, c_i32, c_i32, c_i64, c_i32,
                                          ZbQkNorm, ZbRotation, c_vp, ZbRows, c_vp, ZbRows, c_vp, c_vp, c_vp, c_vp,
                                          c_vp, c_sz, c_vp]),
+    "zb_kv8_append": (c_i32, [ZbKv8, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "zb_kv8_read": (c_i32, [ZbKv8, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "zb_kv8_attn_workspace_bytes": (c_sz, [ZbKv8, c_i32, c_i64, c_i32]),
+    "zb_kv8_attn": (c_i32, [c_vp, c_i32, c_i64, ZbKv8, c_vp, c_i32, c_f32, c_vp, c_vp, c_i32, c_vp, c_sz, c_vp]),
+    "zb_kv8_evict": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]),
     "zb_last_device_status": (c_i32, [c_vp]),
 }
 

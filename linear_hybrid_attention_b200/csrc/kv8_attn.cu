@@ -1,0 +1,730 @@
+// Softmax attention over the 8-bit key/value cache for few query rows a head
+// (decoding), and the join of partial results.
+//
+//   x_rj = scale q_r . code_j s_k[block of j],   p = softmax over the row's keys,
+//   O_r = sum_j p_rj s_v[block of j] code_j,     weight of block b = sum of p over
+//   its keys and the head's rows.
+//
+// Bound by the cache's bytes (128 a token): every byte is read once.  Work is cut
+// into chunks of 64 keys, laid end to end over all heads (and 16-row tiles of
+// their queries), and each CTA takes an equal run of chunks, whatever the heads'
+// lengths; lengths are read on the device, so a captured graph serves all of them.
+// Each of the 8 warps of a CTA streams chunks of its own through a ring of
+// STAGES bulk copies (4 KB of keys, 4 KB of values each): no barrier is shared
+// between warps but at the end of a head's run, where the CTA joins their partial
+// sums.  A run that is not the whole of a head goes to the workspace, and the join
+// kernel adds the runs up.
+//
+// The codes go to the matrix instruction as fp16, which holds both formats
+// exactly; the scales stay in fp32 (s_k multiplies the logits, s_v the chunk's
+// product).  Queries are scaled by a power of two per row to fp16's range.  The
+// features and keys a lane holds are chosen so that it reads its 16 bytes of a key
+// and its 8 bytes of four values in one piece each.
+#include <cuda_runtime.h>
+
+#include "kv8.cuh"
+
+namespace zb {
+namespace kv8 {
+
+constexpr int WARPS = 8;
+constexpr int STAGES = 3;
+constexpr int TILE = 16;                         // query rows of an item
+constexpr uint32_t HALF_STAGE = CHUNK * HD;      // 4 KB of codes
+
+struct AttnArgs {
+    zb_kv8 c;
+    const uint16_t* Q;
+    uint16_t* O;
+    float* lse;
+    const int32_t* lens;
+    int rows, n_q, tiles;        // query rows a head (its group's heads x n_q), items a head
+    int causal;
+    float scale_log2;
+    int groups;                  // weight sums a head: runs of min(block, 64) keys, or 0
+    // workspace
+    float* part_o;               // [slots of partial runs][TILE][64]
+    float2* part_ml;             // [...][TILE]: running maximum (log2 units) and sum
+    int2* item;                  // [heads * tiles]: first partial run, number of runs
+    float* gsum;                 // [heads][groups][rows]: log2 of a row's sum over a group
+    float* lse2;                 // [heads][rows]: log2 of a row's whole sum (more than JOIN_ROWS rows)
+    int* status;
+    unsigned long long timeout_ns;
+};
+
+struct __align__(128) AttnSmem {
+    uint8_t ring[WARPS][STAGES][2][HALF_STAGE];
+    float o[WARPS][TILE][HD];
+    float m[WARPS][TILE], l[WARPS][TILE];
+    uint64_t full[WARPS][STAGES];
+    unsigned long long wsum[WARPS];
+    long long total, start_before;
+    int start_head;
+    int abort_flag;
+};
+
+// Where a warp stands in the CTA's run [at, end): the current item and the chunks
+// of it that fall into the run.
+struct Cursor {
+    int h, tile;
+    int c, c1;            // next chunk of this warp, end of the item's part
+    int c0;               // first chunk of the item's part
+    int nc;               // chunks of the item
+    long long left;       // chunks of the run after this part
+};
+
+ZB_DEVINL int chunks_of(long long len) { return static_cast<int>((len + CHUNK - 1) / CHUNK); }
+
+// ROWS8: the item has at most 8 rows, the other half of the tile is not computed.
+// GK: 16-key steps that share a value scale (block / 16, at most 4).
+template <int FMT, bool ROWS8, int GK>
+__global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    AttnSmem& sm = *reinterpret_cast<AttnSmem*>(smem_raw);
+    const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c4 = lane & 3;
+    const zb_kv8& c = a.c;
+    const int B = c.block, shift = 31 - __clz(B);
+    const long long cap = static_cast<long long>(c.slots) * B;
+    constexpr int PIECES = 4 / GK;                  // blocks a chunk spans
+    constexpr int PIECE_ROWS = CHUNK / PIECES;
+    constexpr uint32_t PIECE_BYTES = PIECE_ROWS * HD;
+
+    // ---- this CTA's run: chunk counts of all heads, end to end -------------
+    const int per = (c.heads + WARPS * 32 - 1) / (WARPS * 32);
+    const int ha = min(static_cast<int>(threadIdx.x) * per, c.heads), hb = min(ha + per, c.heads);
+    long long mine = 0;
+    for (int h = ha; h < hb; ++h) mine += static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    if (threadIdx.x == 0) sm.abort_flag = 0;
+    if (lane == 0)
+        for (int s = 0; s < STAGES; ++s) mbar_init(smem_addr(&sm.full[warp][s]), 1);
+    fence_mbar_init();
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sm.wsum[w];
+        total += sm.wsum[w];
+    }
+    const long long ctas = min(static_cast<long long>(gridDim.x), total);
+    if (blockIdx.x >= ctas) return;
+    const long long at = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+    if (before <= at && at < before + mine) {
+        long long b = before;
+        for (int h = ha; h < hb; ++h) {
+            const long long n = static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+            if (at < b + n) {
+                sm.start_head = h;
+                sm.start_before = b;
+                break;
+            }
+            b += n;
+        }
+    }
+    __syncthreads();
+
+    auto open = [&](Cursor& k, int h, long long into, long long left) {
+        // position `into` of head h's chunks, `left` chunks to go in the run
+        k.h = h;
+        k.nc = chunks_of(head_len(a.lens, h, cap));
+        k.tile = static_cast<int>(into / k.nc);
+        k.c0 = static_cast<int>(into - static_cast<long long>(k.tile) * k.nc);
+        const long long here = min(left, static_cast<long long>(k.nc - k.c0));
+        k.c1 = k.c0 + static_cast<int>(here);
+        k.c = k.c0 + warp;
+        k.left = left - here;
+    };
+    auto next_part = [&](Cursor& k) -> bool {       // the run's next item
+        if (k.left == 0) return false;
+        int h = k.h, t = k.tile + 1;
+        if (t == a.tiles) {
+            t = 0;
+            do ++h; while (chunks_of(head_len(a.lens, h, cap)) == 0);
+        }
+        open(k, h, static_cast<long long>(t) * chunks_of(head_len(a.lens, h, cap)), k.left);
+        return true;
+    };
+    Cursor cur, iss;
+    open(cur, sm.start_head, at - sm.start_before, end - at);
+    iss = cur;
+    bool more = true;                                // the issue cursor stands on a part
+    auto settle = [&]() {                            // move the issue cursor to this warp's next chunk
+        while (more && iss.c >= iss.c1) more = next_part(iss);
+    };
+    settle();
+
+    const WaitCtx wc{a.status, &sm.abort_flag, a.timeout_ns};
+    uint8_t(*ring)[2][HALF_STAGE] = sm.ring[warp];
+    uint32_t issued = 0, used = 0;
+    float ks_q[STAGES], vs_q[STAGES];                // scales of the chunks in the ring (lane: piece)
+    for (int s = 0; s < STAGES; ++s) ks_q[s] = vs_q[s] = 0.f;
+    float ks_new = 0.f, vs_new = 0.f;
+    bool dead = false;
+
+    // Start the copies of the issue cursor's chunk; its scales land in ks_new, vs_new.
+    auto issue = [&]() {
+        const long long len = head_len(a.lens, iss.h, cap);
+        const long long key0 = static_cast<long long>(iss.c) * CHUNK;
+        const int have = static_cast<int>((min(len - key0, static_cast<long long>(CHUNK)) + PIECE_ROWS - 1) / PIECE_ROWS);
+        const int s = issued % STAGES;
+        const uint32_t bar = smem_addr(&sm.full[warp][s]);
+        ks_new = vs_new = 0.f;
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have) * 2 * PIECE_BYTES);
+        __syncwarp();
+        if (lane < have) {
+            const long long key = key0 + lane * PIECE_ROWS;
+            const int slot = slot_of(c, iss.h, key >> shift, a.status);
+            const long long blk = static_cast<long long>(iss.h) * c.slots + slot;
+            const long long byte = (blk * B + (key & (B - 1))) * HD;
+            bulk_load(smem_addr(&ring[s][0][lane * PIECE_BYTES]), c.k + byte, PIECE_BYTES, bar);
+            bulk_load(smem_addr(&ring[s][1][lane * PIECE_BYTES]), c.v + byte, PIECE_BYTES, bar);
+            ks_new = __ldg(c.k_scale + blk);
+            vs_new = __ldg(c.v_scale + blk);
+        }
+        ++issued;
+        iss.c += WARPS;
+        settle();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+        if (more) {
+            issue();
+            ks_q[s] = ks_new;
+            vs_q[s] = vs_new;
+        }
+    }
+
+    bool running = true;
+    while (running) {
+        // ---- one item's part of the run ------------------------------------
+        const long long len = head_len(a.lens, cur.h, cap);
+        const int row0 = cur.tile * TILE, live_rows = min(TILE, a.rows - row0);
+        const uint16_t* Q = a.Q + (static_cast<long long>(cur.h) * a.rows + row0) * HD;
+        uint32_t qa[4][4];
+        float qf[2];
+        long long lim[2];                            // keys the thread's two rows see
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = g + 8 * u;
+            float f[16];
+            uint32_t top = 0;
+            uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (r < live_rows && !(ROWS8 && u)) {
+                w[0] = __ldg(reinterpret_cast<const uint4*>(Q + r * HD) + c4 * 2);
+                w[1] = __ldg(reinterpret_cast<const uint4*>(Q + r * HD) + c4 * 2 + 1);
+            }
+            const uint32_t ww[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[2 * i] = bf16_lo(ww[i]);
+                f[2 * i + 1] = bf16_hi(ww[i]);
+                top = max(top, max((ww[i] & 0x7FFFu) << 16, ww[i] & 0x7FFF0000u));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // row largest to [2^14, 2^15): exact in fp16 down to 2^-28 of it, and to 2^-39 of it below
+            int e = static_cast<int>(top >> 23) - 127;
+            e = max(e, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+            // a row that is not finite has NaN logits throughout
+            qf[u] = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : down * a.scale_log2;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float z = top >= 0x7F800000u ? 0.f : up;
+                qa[s][u] = pack_f16x2(f[4 * s] * z, f[4 * s + 1] * z);
+                qa[s][2 + u] = pack_f16x2(f[4 * s + 2] * z, f[4 * s + 3] * z);
+            }
+            lim[u] = a.causal ? len - a.n_q + 1 + (row0 + r) % a.n_q : len;
+        }
+        float o[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        for (; cur.c < cur.c1; cur.c += WARPS) {
+            const int st = used % STAGES;
+            if (!dead && !mbar_wait_warp(smem_addr(&sm.full[warp][st]), (used / STAGES) & 1, wc)) dead = true;
+            if (dead) break;                         // nothing more is issued; drained below
+            ++used;
+            const float ksl = ks_q[0], vsl = vs_q[0];
+            const long long key0 = static_cast<long long>(cur.c) * CHUNK;
+            const uint8_t* kc = ring[st][0];
+            uint8_t* vc = ring[st][1];
+            // keys of the chunk that each row sees: all of them but at a head's end
+            const int end0 = static_cast<int>(max(min(lim[0] - key0, 64ll), 0ll));
+            const int end1 = static_cast<int>(max(min(lim[1] - key0, 64ll), 0ll));
+            const int valid = static_cast<int>(min(len - key0, 64ll));
+            const bool edge = __any_sync(0xffffffffu, end0 < CHUNK || end1 < CHUNK);
+            if (valid < CHUNK) {
+                // rows behind the last token: what the ring held before could be any code
+                for (int i = valid * (HD / 8) + lane; i < CHUNK * HD / 8; i += 32)
+                    reinterpret_cast<uint2*>(vc)[i] = make_uint2(0, 0);
+                fence_proxy_async_smem();            // before a later copy into this stage
+                __syncwarp();
+            }
+            // ---- logits: key (nt, n) of the instruction is row 16 (nt / 2) + 8 (nt & 1) + 4 (n & 1) + n / 2
+            float x[8][4];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const int key = 16 * (nt >> 1) + 8 * (nt & 1) + 4 * (g & 1) + (g >> 1);
+                const uint4 w = *reinterpret_cast<const uint4*>(kc + key * HD + c4 * 16);
+                x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t b0, b1;
+                    unpack4<FMT>(ww[s], b0, b1);
+                    mma_f16(x[nt], qa[s], b0, b1);
+                }
+            }
+            // ---- softmax over the chunk ------------------------------------
+            constexpr int US = ROWS8 ? 1 : 2;
+            float mx[2] = {m[0], m[1]};
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float ks = PIECES == 1 ? __shfl_sync(0xffffffffu, ksl, 0)
+                                             : __shfl_sync(0xffffffffu, ksl, (nt >> 1) / GK);
+#pragma unroll
+                for (int u = 0; u < US; ++u) {
+                    const float f = ks * qf[u];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = x[nt][2 * u + e] * f;
+                        if (edge) {                  // this lane's columns 2 c4 + e
+                            const int key = 16 * (nt >> 1) + 8 * (nt & 1) + 4 * e + c4;
+                            v = key < (u ? end1 : end0) ? v : -INFINITY;
+                        }
+                        x[nt][2 * u + e] = v;
+                        mx[u] = fmaxf(mx[u], v);
+                    }
+                }
+            }
+            float corr[2] = {1.f, 1.f}, ref[2];
+#pragma unroll
+            for (int u = 0; u < US; ++u) {
+                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+                ref[u] = mx[u] == -INFINITY ? 0.f : mx[u] - P_SHIFT;
+                corr[u] = m[u] == -INFINITY ? 0.f : ex2(m[u] - mx[u]);
+                m[u] = mx[u];
+                l[u] *= corr[u];
+            }
+            uint32_t pa[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    pa[t][u] = pa[t][2 + u] = 0u;
+                    if (u < US) {
+                        const float p0 = ex2(x[2 * t][2 * u] - ref[u]), p1 = ex2(x[2 * t][2 * u + 1] - ref[u]);
+                        const float p2 = ex2(x[2 * t + 1][2 * u] - ref[u]), p3 = ex2(x[2 * t + 1][2 * u + 1] - ref[u]);
+                        pa[t][u] = pack_f16x2(p0, p1);
+                        pa[t][2 + u] = pack_f16x2(p2, p3);
+                        x[2 * t][2 * u] = (p0 + p1) + (p2 + p3);   // the step's sum, for l and the groups
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < US; ++u)
+                l[u] += (x[0][2 * u] + x[2][2 * u]) + (x[4][2 * u] + x[6][2 * u]);
+            if (a.groups) {
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+#pragma unroll
+                    for (int u = 0; u < US; ++u) {
+                        float s = 0.f;
+#pragma unroll
+                        for (int t = p * GK; t < (p + 1) * GK; ++t) s += x[2 * t][2 * u];
+                        s += __shfl_xor_sync(0xffffffffu, s, 1);
+                        s += __shfl_xor_sync(0xffffffffu, s, 2);
+                        const int r = g + 8 * u;
+                        const long long grp = (key0 >> 6) * PIECES + p;
+                        if (c4 == 0 && r < live_rows && grp < a.groups)
+                            a.gsum[(static_cast<long long>(cur.h) * a.groups + grp) * a.rows + row0 + r] =
+                                log2f(s) + ref[u];
+                    }
+                }
+            }
+            // ---- values: lane's output features are 8 g ... (columns) of tile j: feature 8 n + j
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j][0] *= corr[0];
+                o[j][1] *= corr[0];
+                o[j][2] *= corr[1];
+                o[j][3] *= corr[1];
+            }
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                float acc[8][4];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+                for (int t = p * GK; t < (p + 1) * GK; ++t) {
+                    uint2 w[4];                      // rows 16 t + 4 i + c4: keys (2t, 2 c4), (2t, 2 c4 + 1), (2t + 1, ...)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = *reinterpret_cast<const uint2*>(vc + (16 * t + 4 * i + c4) * HD + g * 8);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {    // four features at a time
+                        const uint32_t a0 = i ? w[0].y : w[0].x, a1 = i ? w[1].y : w[1].x;
+                        const uint32_t a2 = i ? w[2].y : w[2].x, a3 = i ? w[3].y : w[3].x;
+                        uint32_t b0[4], b1[4];
+                        unpack4<FMT>(prmt(a0, a1, 0x5140u), b0[0], b0[1]);
+                        unpack4<FMT>(prmt(a0, a1, 0x7362u), b0[2], b0[3]);
+                        unpack4<FMT>(prmt(a2, a3, 0x5140u), b1[0], b1[1]);
+                        unpack4<FMT>(prmt(a2, a3, 0x7362u), b1[2], b1[3]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma_f16(acc[i * 4 + q], pa[t], b0[q], b1[q]);
+                    }
+                }
+                const float vs = __shfl_sync(0xffffffffu, vsl, p);
+                // a row that sees nothing of the piece takes nothing of it, whatever its scale is
+                const float v0 = end0 > p * PIECE_ROWS ? vs : 0.f, v1 = end1 > p * PIECE_ROWS ? vs : 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    o[j][0] = fmaf(acc[j][0], v0, o[j][0]);
+                    o[j][1] = fmaf(acc[j][1], v0, o[j][1]);
+                    o[j][2] = fmaf(acc[j][2], v1, o[j][2]);
+                    o[j][3] = fmaf(acc[j][3], v1, o[j][3]);
+                }
+            }
+            __syncwarp();                            // the stage has been read
+            // ---- next copy into the stage, and the scales move up ----------
+#pragma unroll
+            for (int s = 0; s + 1 < STAGES; ++s) {
+                ks_q[s] = ks_q[s + 1];
+                vs_q[s] = vs_q[s + 1];
+            }
+            ks_new = vs_new = 0.f;
+            if (more) issue();
+            ks_q[STAGES - 1] = ks_new;
+            vs_q[STAGES - 1] = vs_new;
+        }
+
+        // ---- join the warps' partial results of the part --------------------
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+            const int r = g + 8 * u;
+            if (c4 == 0) {
+                sm.m[warp][r] = m[u];
+                sm.l[warp][r] = l[u];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {            // features 16 c4 + 8 e + j
+                float4* d = reinterpret_cast<float4*>(&sm.o[warp][r][16 * c4 + 8 * e]);
+                d[0] = make_float4(o[0][2 * u + e], o[1][2 * u + e], o[2][2 * u + e], o[3][2 * u + e]);
+                d[1] = make_float4(o[4][2 * u + e], o[5][2 * u + e], o[6][2 * u + e], o[7][2 * u + e]);
+            }
+        }
+        __syncthreads();
+        const long long it = static_cast<long long>(cur.h) * a.tiles + cur.tile;
+        const long long run = it + blockIdx.x;
+        const bool whole = cur.c0 == 0 && cur.c1 == cur.nc;
+        for (int i = threadIdx.x; i < live_rows * (HD / 4); i += WARPS * 32) {
+            const int r = i / (HD / 4), q = i % (HD / 4);
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.m[w][r]);
+            float L = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float f = sm.m[w][r] == -INFINITY ? 0.f : ex2(sm.m[w][r] - M);
+                const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][r][4 * q]);
+                L = fmaf(sm.l[w][r], f, L);
+                s.x = fmaf(v.x, f, s.x);
+                s.y = fmaf(v.y, f, s.y);
+                s.z = fmaf(v.z, f, s.z);
+                s.w = fmaf(v.w, f, s.w);
+            }
+            if (q == 0) a.part_ml[run * TILE + r] = make_float2(M, L);
+            if (whole) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;   // no key: zeros; NaN stays
+                const long long row = static_cast<long long>(cur.h) * a.rows + row0 + r;
+                reinterpret_cast<uint2*>(a.O + row * HD)[q] =
+                    make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
+                if (q == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M - P_SHIFT + log2f(L)) * LN2;
+            } else {
+                reinterpret_cast<float4*>(a.part_o + (run * TILE + r) * HD)[q] = s;
+            }
+        }
+        if (threadIdx.x == 0 && cur.c0 == 0) {
+            // the runs of this item: CTAs from this one to the one with its last chunk
+            const long long last = (at + (end - at - cur.left) - cur.c1 + cur.nc) - 1;   // its place in all chunks
+            const long long to = ((last + 1) * ctas - 1) / total;
+            a.item[it] = make_int2(static_cast<int>(run), static_cast<int>(to - blockIdx.x + 1));
+        }
+        __syncthreads();                             // sm.o is free again
+        running = next_part(cur);
+    }
+    // copies of a warp that gave up are still writing its ring
+    for (; used < issued; ++used) {
+        const WaitCtx drain{a.status, &sm.abort_flag, drain_timeout_ns(a.timeout_ns)};
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_addr(&sm.full[warp][used % STAGES]), (used / STAGES) & 1))
+            if (globaltimer_ns() - t0 > drain.timeout_ns) break;
+    }
+}
+
+// ------------------------------------------------------------------ join ----
+// Adds up the partial runs of each item (rows without a token: zeros, -inf) and,
+// with a.groups, turns the rows' group sums into the blocks' weight.  Grid: (heads,
+// parts): every part works out the rows' log-sum-exp again, part 0 writes the
+// outputs, and the blocks are shared out over the parts.
+constexpr int JOIN_ROWS = 32;
+__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
+    __shared__ float lse2[JOIN_ROWS];
+    const zb_kv8& c = a.c;
+    const int h = blockIdx.x, part = blockIdx.y;
+    const long long cap = static_cast<long long>(c.slots) * c.block;
+    const long long len = head_len(a.lens, h, cap);
+    if (len == 0) {
+        if (part) return;
+        for (int i = threadIdx.x; i < a.rows * (HD / 8); i += 256) {
+            const long long row = static_cast<long long>(h) * a.rows + i / (HD / 8);
+            reinterpret_cast<uint4*>(a.O + row * HD)[i % (HD / 8)] = make_uint4(0, 0, 0, 0);
+            if (i % (HD / 8) == 0 && a.lse) a.lse[row] = -INFINITY;
+        }
+        return;
+    }
+    // 16 threads a row, 4 features each
+    const int r = threadIdx.x >> 4, q = threadIdx.x & 15;
+    for (int r0 = 0; r0 < a.rows; r0 += 16) {
+        const int row = r0 + r;
+        if (row < a.rows) {
+            const int2 it = a.item[static_cast<long long>(h) * a.tiles + row / TILE];
+            const int rr = row % TILE;
+            float M = -INFINITY;
+            for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[static_cast<long long>(it.x + i) * TILE + rr].x);
+            float L = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < it.y; ++i) {
+                const long long at = static_cast<long long>(it.x + i) * TILE + rr;
+                const float2 ml = a.part_ml[at];
+                if (ml.y == 0.f) continue;
+                const float f = ex2(ml.x - M);
+                L = fmaf(ml.y, f, L);
+                if (part == 0 && it.y > 1) {
+                    const float4 v = reinterpret_cast<const float4*>(a.part_o + at * HD)[q];
+                    s.x = fmaf(v.x, f, s.x);
+                    s.y = fmaf(v.y, f, s.y);
+                    s.z = fmaf(v.z, f, s.z);
+                    s.w = fmaf(v.w, f, s.w);
+                }
+            }
+            const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
+            if (q == 0) lse2[row] = t;
+            if (part == 0 && it.y > 1) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const long long out = static_cast<long long>(h) * a.rows + row;
+                reinterpret_cast<uint2*>(a.O + out * HD)[q] =
+                    make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
+                if (q == 0 && a.lse) a.lse[out] = t * LN2;
+            }
+        }
+    }
+    if (!a.groups) return;
+    __syncthreads();
+    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
+    const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
+    const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
+    for (int b = part * 256 + threadIdx.x; b < blocks; b += gridDim.y * 256) {
+        float s = 0.f;
+        for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
+            const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
+            for (int i = 0; i < a.rows; ++i)
+                if (lse2[i] != -INFINITY) s += ex2(gs[i] - lse2[i]);
+        }
+        const int slot = slot_of(c, h, b, a.status);
+        c.mass[static_cast<long long>(h) * c.slots + slot] += s;
+    }
+}
+
+// The same for more rows, in two launches: the rows of one item a CTA, then a warp
+// a block for the weights (a head's rows are contiguous in its group sums).
+template <int TR>
+__global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
+    const zb_kv8& c = a.c;
+    const int h = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+    const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
+    const int2 it = len ? a.item[blockIdx.x] : make_int2(0, 0);
+    const int q = threadIdx.x & 15;
+    for (int r = threadIdx.x >> 4; r < TR && tile * TR + r < a.rows; r += 16) {
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[static_cast<long long>(it.x + i) * TR + r].x);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < it.y; ++i) {
+            const long long at = static_cast<long long>(it.x + i) * TR + r;
+            const float2 ml = a.part_ml[at];
+            if (ml.y == 0.f) continue;
+            const float f = ex2(ml.x - M);
+            L = fmaf(ml.y, f, L);
+            if (it.y > 1) {
+                const float4 v = reinterpret_cast<const float4*>(a.part_o + at * HD)[q];
+                s.x = fmaf(v.x, f, s.x);
+                s.y = fmaf(v.y, f, s.y);
+                s.z = fmaf(v.z, f, s.z);
+                s.w = fmaf(v.w, f, s.w);
+            }
+        }
+        const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
+        const long long row = static_cast<long long>(h) * a.rows + tile * TR + r;
+        if (q == 0 && a.lse2) a.lse2[row] = t;
+        if (it.y != 1) {                             // an item of one run has been written already
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            reinterpret_cast<uint2*>(a.O + row * HD)[q] =
+                make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
+            if (q == 0 && a.lse) a.lse[row] = t * LN2;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
+    const zb_kv8& c = a.c;
+    const int h = blockIdx.x;
+    const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
+    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
+    const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
+    const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
+    const float* lse2 = a.lse2 + static_cast<long long>(h) * a.rows;
+    for (int b = blockIdx.y * 8 + warp_id(); b < blocks; b += gridDim.y * 8) {
+        float s = 0.f;
+        for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
+            const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
+            for (int i = lane_id(); i < a.rows; i += 32) {
+                const float t = __ldg(lse2 + i);
+                if (t != -INFINITY) s += ex2(gs[i] - t);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane_id() == 0) {
+            const int slot = slot_of(c, h, b, a.status);
+            c.mass[static_cast<long long>(h) * c.slots + slot] += s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host ----
+struct Plan {
+    long long rows, tiles, runs, groups;
+    size_t o, ml, item, gsum, lse2, total;
+};
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+constexpr int MAX_SMS = 256;
+
+Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
+    Plan p{};
+    p.rows = static_cast<long long>(heads_q / c.heads) * n_q;
+    p.tiles = (p.rows + TILE - 1) / TILE;
+    p.runs = p.tiles * c.heads + MAX_SMS;
+    p.groups = add_mass ? static_cast<long long>(c.slots) * (c.block > CHUNK ? c.block / CHUNK : 1) : 0;
+    p.o = up256(static_cast<size_t>(p.runs) * TILE * HD * sizeof(float));
+    p.ml = up256(static_cast<size_t>(p.runs) * TILE * sizeof(float2));
+    p.item = up256(static_cast<size_t>(p.tiles) * c.heads * sizeof(int2));
+    p.gsum = up256(static_cast<size_t>(p.groups) * c.heads * p.rows * sizeof(float));
+    p.lse2 = p.rows > JOIN_ROWS && add_mass ? up256(static_cast<size_t>(c.heads) * p.rows * sizeof(float)) : 0;
+    p.total = p.o + p.ml + p.item + p.gsum + p.lse2;
+    return p;
+}
+
+template <int FMT, bool ROWS8, int GK>
+zb_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
+    auto* fn = attn_kernel<FMT, ROWS8, GK>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnSmem)) != cudaSuccess)
+        return ZB_ERR_CUDA;
+    fn<<<ctas, WARPS * 32, sizeof(AttnSmem), st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}
+template <int FMT, bool ROWS8>
+zb_status launch_block(const AttnArgs& a, int ctas, cudaStream_t st) {
+    switch (a.c.block) {
+        case 16: return launch_attn<FMT, ROWS8, 1>(a, ctas, st);
+        case 32: return launch_attn<FMT, ROWS8, 2>(a, ctas, st);
+        default: return launch_attn<FMT, ROWS8, 4>(a, ctas, st);
+    }
+}
+template <int FMT>
+zb_status launch_rows(const AttnArgs& a, int ctas, cudaStream_t st) {
+    return a.rows <= 8 ? launch_block<FMT, true>(a, ctas, st) : launch_block<FMT, false>(a, ctas, st);
+}
+
+}  // namespace kv8
+}  // namespace zb
+
+using namespace zb;
+
+extern "C" size_t zb_kv8_attn_workspace_bytes(zb_kv8 cache, int32_t heads_q, int64_t n_q, int32_t add_mass) {
+    if (kv8::check_cache(cache, false) != ZB_OK || heads_q < 1 || heads_q % cache.heads || n_q < 1) return 0;
+    return kv8::plan(cache, heads_q, n_q, add_mass).total;
+}
+
+extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q, zb_kv8 cache, const int32_t* lens,
+                                 int32_t causal, float scale, uint16_t* O, float* lse, int32_t add_mass, void* ws,
+                                 size_t ws_bytes, void* stream) {
+    zb_status e = kv8::check_cache(cache, true);
+    if (e != ZB_OK) return e;
+    if (heads_q < 1 || heads_q % cache.heads || n_q < 1) return ZB_ERR_SHAPE;
+    if (!(scale > 0.f) || !(scale <= 3.4e38f)) return ZB_ERR_SHAPE;
+    if (n_q > 0x7FFFFFFFll || static_cast<long long>(heads_q / cache.heads) * n_q > 0x7FFFFFFFll) return ZB_ERR_UNSUPPORTED;
+    if (!Q || !lens || !O || (add_mass && !cache.mass)) return ZB_ERR_NULL;
+    if (!aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return ZB_ERR_ALIGN;
+    const kv8::Plan p = kv8::plan(cache, heads_q, n_q, add_mass);
+    if (!ws || ws_bytes < p.total) return ZB_ERR_WORKSPACE;
+    if (!aligned16(ws)) return ZB_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((e = current_device(&dev)) != ZB_OK) return e;
+    if (dev.sm_count > kv8::MAX_SMS) return ZB_ERR_DEVICE;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    kv8::AttnArgs a{};
+    a.c = cache;
+    a.Q = Q;
+    a.O = O;
+    a.lse = lse;
+    a.lens = lens;
+    a.rows = static_cast<int>(p.rows);
+    a.n_q = static_cast<int>(n_q);
+    a.tiles = static_cast<int>(p.tiles);
+    a.causal = causal != 0;
+    a.scale_log2 = scale * kv8::LOG2E;
+    a.groups = static_cast<int>(p.groups);
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float2*>(w + p.o);
+    a.item = reinterpret_cast<int2*>(w + p.o + p.ml);
+    a.gsum = reinterpret_cast<float*>(w + p.o + p.ml + p.item);
+    a.status = dev.status;
+    a.timeout_ns = wait_timeout_ns();
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    e = cache.format == ZB_KV8_INT8 ? kv8::launch_rows<ZB_KV8_INT8>(a, dev.sm_count, st)
+                                    : kv8::launch_rows<ZB_KV8_E4M3>(a, dev.sm_count, st);
+    if (e != ZB_OK) return e;
+    if (p.rows > kv8::JOIN_ROWS) {
+        if (add_mass) a.lse2 = reinterpret_cast<float*>(w + p.o + p.ml + p.item + p.gsum);
+        kv8::join_rows_kernel<kv8::TILE><<<static_cast<unsigned>(cache.heads * p.tiles), 256, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
+        if (add_mass) {
+            const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
+            kv8::mass_kernel<<<dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)), 256, 0, st>>>(a);
+        }
+        return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+    }
+    int parts = 1;
+    if (a.groups) {
+        parts = (cache.slots + 255) / 256;
+        if (parts > 64) parts = 64;
+    }
+    kv8::join_kernel<<<dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)), 256, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}

@@ -1,0 +1,484 @@
+// The 8-bit key/value cache: append, read back, evict.
+//
+// A head's cache is a list of blocks of B tokens (16 to 128).  Codes of a block
+// share one scale for its keys and one for its values,
+//   s = max|x| / M  (M = 127 for int8, 448 for e4m3; fp32, rounded to nearest),
+//   code = the nearest to x / s (of two as near, the even one),
+// and a block holding a value that is not finite gets s = NaN and reads as NaN.
+// The block in progress keeps its original bf16 rows beside the codes (`tail`)
+// and is quantised again whenever rows join it, so what the cache holds does not
+// depend on how tokens were split over calls.  A table maps logical blocks to
+// slots; eviction only reorders it: kept blocks move up, freed slots go behind
+// them for later appends, and no code is touched.
+//
+// Rounding is decided exactly.  x / s in fp32 may land on a tie that the exact
+// quotient misses by less than its rounding; where the quotient is that near a
+// tie (one value in some ten thousand), the sign of the fused x - (k + 1/2) s,
+// which no rounding can change, decides.
+#include <cuda_runtime.h>
+
+#include "kv8.cuh"
+
+namespace zb {
+namespace kv8 {
+
+constexpr int UNIT = 128;      // rows an append CTA takes: a multiple of every block size
+constexpr int A_THREADS = 256;
+
+// ---------------------------------------------------------- quantisation ----
+// Whole number nearest to x / s, ties to even; inv ~ 1 / s.
+ZB_DEVINL float exact_round(float x, float s, float t) {
+    const float k = floorf(t);
+    const float r = fmaf(-(k + 0.5f), s, x);
+    const bool odd = (static_cast<int>(k) & 1) != 0;
+    return k + ((r > 0.f || (r == 0.f && odd)) ? 1.f : 0.f);
+}
+
+ZB_DEVINL float quotient(float x, float s, float inv) {
+    // 1 / s overflows for a scale that is itself subnormal or nearly so
+    return s < 0x1p-120f ? x / s : x * inv;
+}
+
+ZB_DEVINL int code_int8(float x, float s, float inv) {
+    const float t = quotient(x, s, inv);
+    float q = rintf(t);
+    if (fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = exact_round(x, s, t);
+    q = fminf(fmaxf(q, -127.f), 127.f);
+    return static_cast<int>(q);
+}
+
+// The value of the e4m3 code nearest to x / s.
+ZB_DEVINL float value_e4m3(float x, float s, float inv) {
+    const float t = quotient(x, s, inv);
+    const uint32_t bits = __float_as_uint(t) & 0x7FFFFFFFu;
+    const int off = static_cast<int>(bits & 0xFFFFFu) - 0x80000;
+    // off the grid's ties by more than the quotient's error: the conversion is exact
+    if (bits >= 0x3C800000u && (off > 256 || off < -256)) return t;
+    if (bits == 0u) return t;
+    int e = static_cast<int>(bits >> 23) - 127;
+    if (e < -6) e = -6;
+    const float step = __uint_as_float(static_cast<uint32_t>(e - 3 + 127) << 23);
+    const float q = exact_round(fabsf(x), s * step, fabsf(t) / step);
+    return copysignf(fminf(q * step, 448.f), t);
+}
+
+ZB_DEVINL uint32_t pack_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int FMT>
+ZB_DEVINL uint2 codes8(const float* x, float s, float inv) {
+    uint32_t w[2] = {0u, 0u};
+    if (FMT == ZB_KV8_INT8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i >> 2] |= (static_cast<uint32_t>(code_int8(x[i], s, inv)) & 0xFFu) << (8 * (i & 3));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+            w[i >> 2] |= pack_e4m3x2(value_e4m3(x[i], s, inv), value_e4m3(x[i + 1], s, inv)) << (8 * (i & 2));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct AppendArgs {
+    zb_kv8 c;
+    const uint4 *K, *V;
+    int n;
+    const int32_t* lens;
+    int32_t* lens_out;   // NULL: written by a launch of its own
+    int* status;
+};
+
+// One CTA: 128 rows from a block boundary on, of one head, keys and values.  An
+// HBM stream (256 B a token in, 128 B out): each thread has its eight 16-byte
+// loads in flight, a warp takes 16 rows, so a block is a whole number of warps.
+template <int FMT>
+__global__ void __launch_bounds__(A_THREADS) append_kernel(const AppendArgs a) {
+    const int h = blockIdx.y, unit = blockIdx.x;
+    const zb_kv8& c = a.c;
+    const int B = c.block;
+    const long long cap = static_cast<long long>(c.slots) * B;
+    const long long len = __ldg(a.lens + h);
+    if (len < 0 || len + a.n > cap) {          // does not fit: the head stays as it is
+        if (unit == 0 && threadIdx.x == 0) {
+            flag_status(a.status, ZB_ERR_INDEX);
+            if (a.lens_out) a.lens_out[h] = static_cast<int32_t>(len);
+        }
+        return;
+    }
+    const int held = static_cast<int>(len % B);
+    const long long first = len / B;           // logical block that row 0 belongs to
+    const long long rows = held + static_cast<long long>(a.n);
+    const int warp = warp_id(), lane = lane_id();
+    const long long blocks = (rows + B - 1) / B;
+    const long long row0 = static_cast<long long>(unit) * UNIT + warp * 16;
+    const long long blk = row0 / B;            // of this warp
+    const bool live = blk < blocks;
+    const int chunk = lane & 7;
+    uint4* tail[2] = {reinterpret_cast<uint4*>(c.k_tail) + static_cast<long long>(h) * B * 8,
+                      reinterpret_cast<uint4*>(c.v_tail) + static_cast<long long>(h) * B * 8};
+    const uint4* src[2] = {a.K + static_cast<long long>(h) * a.n * 8, a.V + static_cast<long long>(h) * a.n * 8};
+    uint4 x[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long r = row0 + i * 4 + (lane >> 3);
+            x[t][i] = make_uint4(0, 0, 0, 0);
+            if (r < held) x[t][i] = tail[t][r * 8 + chunk];
+            else if (r < rows) x[t][i] = __ldg(src[t] + (r - held) * 8 + chunk);
+        }
+    }
+    // the block's largest magnitude: as integers, so that NaN is above infinity
+    __shared__ uint32_t top[2][A_THREADS / 32];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max(m, max((w[j] & 0x7FFFu) << 16, w[j] & 0x7FFF0000u));
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) top[t][warp] = m;
+    }
+    __syncthreads();
+    if (live) {
+        const int slot = slot_of(c, h, first + blk, a.status);
+        const long long at = static_cast<long long>(h) * c.slots + slot;
+        const int w0 = warp & ~(B / 16 - 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t m = 0;
+            for (int w = w0; w < w0 + B / 16; ++w) m = max(m, top[t][w]);
+            const bool finite = m < 0x7F800000u;
+            const float s = finite ? __fdiv_rn(__uint_as_float(m), FMT == ZB_KV8_INT8 ? 127.f : 448.f)
+                                   : __uint_as_float(0x7FC00000u);
+            const bool codes = finite && s > 0.f;
+            const float inv = codes ? 1.f / s : 0.f;
+            uint2* out = reinterpret_cast<uint2*>(t ? c.v : c.k) + at * B * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8];
+                const uint32_t w[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = bf16_lo(w[j]);
+                    f[2 * j + 1] = bf16_hi(w[j]);
+                }
+                const long long r = row0 + i * 4 + (lane >> 3) - blk * B;
+                out[r * 8 + chunk] = codes ? codes8<FMT>(f, s, inv) : make_uint2(0, 0);
+            }
+            if (warp == w0 && lane == 0) (t ? c.v_scale : c.k_scale)[at] = s;
+        }
+        // a block that this call opens starts without weight
+        if (c.mass && warp == w0 && lane == 0 && (blk > 0 || held == 0)) c.mass[at] = 0.f;
+    }
+    if (unit == 0) {
+        // The rows of the block left in progress, once this CTA has read the old
+        // ones (no other CTA reads them: they are all in the first unit).
+        __syncthreads();
+        const int left = static_cast<int>(rows % B);
+        const long long last = rows - left;
+        for (int i = threadIdx.x; i < left * 8; i += A_THREADS) {
+            const long long r = last + (i >> 3);
+            if (r < held) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) tail[t][i] = __ldg(src[t] + (r - held) * 8 + (i & 7));
+        }
+        if (threadIdx.x == 0 && a.lens_out) a.lens_out[h] = static_cast<int32_t>(len + a.n);
+    }
+}
+
+// lens + n for the heads whose append fitted (an append over several CTAs a head
+// cannot advance the lengths that its CTAs are reading).
+__global__ void advance_kernel(const int32_t* lens, int32_t* out, int heads, int n, long long cap) {
+    const int h = blockIdx.x * blockDim.x + threadIdx.x;
+    if (h >= heads) return;
+    const long long len = lens[h];
+    out[h] = static_cast<int32_t>(len < 0 || len + n > cap ? len : len + n);
+}
+
+// ------------------------------------------------------------------ read ----
+// The newest n tokens of every head as bf16 (code * scale in fp32, rounded once);
+// rows before a head's first token are zeros.  An HBM stream: 64 B of codes in,
+// 128 B out a row; a thread moves 8 values of one tensor.
+template <int FMT>
+__global__ void __launch_bounds__(256) read_kernel(const zb_kv8 c, const int32_t* lens, int n, uint4* Ko, uint4* Vo,
+                                                   int* status) {
+    const int h = blockIdx.y;
+    const long long cap = static_cast<long long>(c.slots) * c.block;
+    const long long len = head_len(lens, h, cap);
+    const uint8_t* codes = blockIdx.z ? c.v : c.k;
+    const float* scale = blockIdx.z ? c.v_scale : c.k_scale;
+    uint4* out = (blockIdx.z ? Vo : Ko) + static_cast<long long>(h) * n * 8;
+    const int shift = 31 - __clz(c.block);
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < static_cast<long long>(n) * 8;
+         i += static_cast<long long>(gridDim.x) * 256) {
+        const long long tok = len - n + (i >> 3);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (tok >= 0) {
+            const int slot = slot_of(c, h, tok >> shift, status);
+            const long long at = static_cast<long long>(h) * c.slots + slot;
+            const float s = __ldg(scale + at);
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + (at * c.block + (tok & (c.block - 1))) * HD) +
+                                  (i & 7));
+            uint32_t p[4];
+            unpack4<FMT>(w.x, p[0], p[1]);
+            unpack4<FMT>(w.y, p[2], p[3]);
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = half2_floats(p[j]);
+                o[j] = pack_bf16x2(f.x * s, f.y * s);
+            }
+            v = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __stcs(out + i, v);
+    }
+}
+
+// ----------------------------------------------------------------- evict ----
+constexpr int E_THREADS = 1024;
+constexpr int E_BINS = 2048;
+constexpr int E_KEYS = 40960;    // keys kept in shared memory; longer lists gather them again
+
+// Order-preserving key of a weight (NaN with a clear sign above +inf; -0 as +0).
+ZB_DEVINL uint32_t mass_key(float m) {
+    const uint32_t b = m == 0.f ? 0u : __float_as_uint(m);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+struct EvictArgs {
+    const int32_t* table;
+    const float* mass;
+    const int32_t* lens;
+    int slots, block, budget, sinks, recent;
+    int32_t *table_out, *lens_out, *kept;
+    int keys_in_smem;
+    int* status;
+};
+
+// One CTA a head.  The blocks between the first `sinks` and the last `recent`
+// are ranked by weight: a histogram over the range the weights span, narrowed
+// to the bin that holds the last kept one until it is a single value (at most
+// three rounds), then one pass that keeps everything above it and the lowest
+// indices among equals, each warp writing its own contiguous part in order.
+// Bound by latency: a few dependent rounds over a list of some thousand words.
+__global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[E_BINS];
+    __shared__ uint32_t red[32], red2[32];
+    __shared__ uint32_t s_lo, s_bin, s_above;
+    const int h = blockIdx.x, tid = threadIdx.x, lane = lane_id(), warp = warp_id();
+    const long long row = static_cast<long long>(h) * a.slots;
+    const int32_t* table = a.table + row;
+    int32_t* out = a.table_out + row;
+    int32_t* kept = a.kept ? a.kept + static_cast<long long>(h) * a.budget : nullptr;
+    const long long len = head_len(a.lens, h, static_cast<long long>(a.slots) * a.block);
+    const int nb = static_cast<int>((len + a.block - 1) / a.block);
+    if (nb <= a.budget) {
+        for (int b = tid; b < a.slots; b += E_THREADS) out[b] = table[b];
+        if (kept)
+            for (int b = tid; b < a.budget; b += E_THREADS) kept[b] = b < nb ? b : -1;
+        if (tid == 0) a.lens_out[h] = static_cast<int32_t>(len);
+        return;
+    }
+    const int b0 = a.sinks, b1 = nb - a.recent;
+    const int need = a.budget - a.sinks - a.recent;   // < b1 - b0
+    auto gather = [&](int b) -> uint32_t {
+        const int s = table[b];
+        if (s < 0 || s >= a.slots) {
+            flag_status(a.status, ZB_ERR_INDEX);
+            return 0u;
+        }
+        return mass_key(a.mass[row + s]);
+    };
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int b = b0 + tid; b < b1; b += E_THREADS) {
+        const uint32_t k = gather(b);
+        if (a.keys_in_smem) keys[b] = k;
+        lo = min(lo, k);
+        hi = max(hi, k);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        red[warp] = lo;
+        red2[warp] = hi;
+    }
+    __syncthreads();
+    lo = __reduce_min_sync(0xffffffffu, red[lane]);
+    hi = __reduce_max_sync(0xffffffffu, red2[lane]);
+    __syncthreads();
+    auto key = [&](int b) -> uint32_t { return a.keys_in_smem ? keys[b] : gather(b); };
+
+    // invariant: `want` keys are to be kept of those in [lo, hi] (the larger ones,
+    // above hi, are all kept already), 0 <= want <= their number
+    uint32_t want = need;
+    while (need > 0 && lo < hi) {
+        const uint32_t span = hi - lo;
+        const int bits = 32 - __clz(span);
+        const int sh = bits > 11 ? bits - 11 : 0;
+        for (int i = tid; i < E_BINS; i += E_THREADS) hist[i] = 0;
+        __syncthreads();
+        for (int b = b0 + tid; b < b1; b += E_THREADS) {
+            const uint32_t k = key(b);
+            if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> sh], 1u);
+        }
+        __syncthreads();
+        // two bins a thread, from the top: the bin where the count reaches `want`
+        const int bin = E_BINS - 2 - 2 * tid;
+        const uint32_t c1 = hist[bin + 1], c0 = hist[bin];
+        uint32_t incl = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        uint32_t before = lane < warp ? red[lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, before) + incl - c0 - c1;   // kept above this thread's bins
+        if (before < want && want <= before + c1) {
+            s_bin = bin + 1;
+            s_above = before;
+        } else if (before + c1 < want && want <= before + c1 + c0) {
+            s_bin = bin;
+            s_above = before + c1;
+        }
+        __syncthreads();
+        want -= s_above;
+        lo += s_bin << sh;
+        const uint32_t width = (1u << sh) - 1u;
+        if (hi - lo > width) hi = lo + width;
+        __syncthreads();
+    }
+    // keep: keys above `hi` (== lo) and the first `want` equal to it
+    const uint32_t edge = need > 0 ? lo : 0xFFFFFFFFu;
+    if (need == 0) want = 0;
+    const int per = ((nb + 1023) / 1024) * 32;            // blocks a warp takes
+    const int w0 = min(warp * per, nb), w1 = min(w0 + per, nb);
+    uint32_t over = 0, ties = 0;
+    for (int b = w0 + lane; b < w1 + ((32 - (w1 - w0) % 32) & 31); b += 32) {
+        const bool in = b < w1, mid = in && b >= b0 && b < b1;
+        const uint32_t k = mid ? key(b) : 0u;
+        over += __popc(__ballot_sync(0xffffffffu, in && (!mid || k > edge)));
+        ties += __popc(__ballot_sync(0xffffffffu, mid && k == edge));
+    }
+    if (lane == 0) {
+        red[warp] = over;
+        red2[warp] = ties;
+    }
+    __syncthreads();
+    const uint32_t over0 = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
+    uint32_t ties0 = __reduce_add_sync(0xffffffffu, lane < warp ? red2[lane] : 0);
+    uint32_t pos = over0 + min(ties0, want);              // kept before this warp's part
+    for (int b = w0 + lane; b < w1 + ((32 - (w1 - w0) % 32) & 31); b += 32) {
+        const bool in = b < w1, mid = in && b >= b0 && b < b1;
+        const uint32_t k = mid ? key(b) : 0u;
+        const uint32_t below = (1u << lane) - 1u;
+        const uint32_t tie = __ballot_sync(0xffffffffu, mid && k == edge);
+        const bool keep = in && (!mid || k > edge || (k == edge && ties0 + __popc(tie & below) < want));
+        const uint32_t mask = __ballot_sync(0xffffffffu, keep);
+        if (in) {
+            const uint32_t r = pos + __popc(mask & below);   // kept blocks before b
+            if (keep) {
+                out[r] = table[b];
+                if (kept) kept[r] = b;
+            } else {
+                out[a.budget + (b - r)] = table[b];
+            }
+        }
+        pos += __popc(mask);
+        ties0 += __popc(tie);
+    }
+    for (int b = nb + tid; b < a.slots; b += E_THREADS) out[b] = table[b];
+    if (tid == 0) a.lens_out[h] = static_cast<int32_t>(len - static_cast<long long>(nb - a.budget) * a.block);
+}
+
+}  // namespace kv8
+}  // namespace zb
+
+using namespace zb;
+
+extern "C" zb_status zb_kv8_append(zb_kv8 cache, const uint16_t* K, const uint16_t* V, int64_t n_new,
+                                   const int32_t* lens, int32_t* lens_out, void* stream) {
+    zb_status e = kv8::check_cache(cache, true);
+    if (e != ZB_OK) return e;
+    if (n_new < 1) return ZB_ERR_SHAPE;
+    if (n_new > static_cast<long long>(cache.slots) * cache.block) return ZB_ERR_SHAPE;
+    if (!K || !V || !lens || !lens_out || !cache.k_tail || !cache.v_tail) return ZB_ERR_NULL;
+    if (!aligned16(K) || !aligned16(V) || !aligned16(cache.k_tail) || !aligned16(cache.v_tail) ||
+        (reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(lens_out) & 3u))
+        return ZB_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((e = current_device(&dev)) != ZB_OK) return e;
+    const long long units = (cache.block - 1 + n_new + kv8::UNIT - 1) / kv8::UNIT;
+    const bool apart = lens == lens_out && units > 1;
+    kv8::AppendArgs a{cache, reinterpret_cast<const uint4*>(K), reinterpret_cast<const uint4*>(V),
+                      static_cast<int>(n_new), lens, apart ? nullptr : lens_out, dev.status};
+    const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(cache.heads));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cache.format == ZB_KV8_INT8) kv8::append_kernel<ZB_KV8_INT8><<<grid, kv8::A_THREADS, 0, st>>>(a);
+    else kv8::append_kernel<ZB_KV8_E4M3><<<grid, kv8::A_THREADS, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
+    if (apart) {
+        kv8::advance_kernel<<<(cache.heads + 255) / 256, 256, 0, st>>>(lens, lens_out, cache.heads,
+                                                                       static_cast<int>(n_new),
+                                                                       static_cast<long long>(cache.slots) * cache.block);
+        if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
+    }
+    return ZB_OK;
+}
+
+extern "C" zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K, uint16_t* V, void* stream) {
+    zb_status e = kv8::check_cache(cache, true);
+    if (e != ZB_OK) return e;
+    if (n < 1 || n > 0x7FFFFFFFll) return ZB_ERR_SHAPE;
+    if (!lens || !K || !V) return ZB_ERR_NULL;
+    if (!aligned16(K) || !aligned16(V) || (reinterpret_cast<uintptr_t>(lens) & 3u)) return ZB_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((e = current_device(&dev)) != ZB_OK) return e;
+    long long gx = (n * 8 + 255) / 256;
+    if (gx > 65536) gx = 65536;
+    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cache.heads), 2);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint4 *ko = reinterpret_cast<uint4*>(K), *vo = reinterpret_cast<uint4*>(V);
+    if (cache.format == ZB_KV8_INT8)
+        kv8::read_kernel<ZB_KV8_INT8><<<grid, 256, 0, st>>>(cache, lens, static_cast<int>(n), ko, vo, dev.status);
+    else
+        kv8::read_kernel<ZB_KV8_E4M3><<<grid, 256, 0, st>>>(cache, lens, static_cast<int>(n), ko, vo, dev.status);
+    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}
+
+extern "C" zb_status zb_kv8_evict(const int32_t* table, const float* mass, const int32_t* lens, int32_t heads,
+                                  int32_t slots, int32_t block, int32_t budget, int32_t sinks, int32_t recent,
+                                  int32_t* table_out, int32_t* lens_out, int32_t* kept, void* stream) {
+    if (heads < 1 || slots < 1 || sinks < 0 || recent < 1) return ZB_ERR_SHAPE;
+    if (block != 16 && block != 32 && block != 64 && block != 128) return ZB_ERR_UNSUPPORTED;
+    if (heads > 65535 || static_cast<long long>(slots) * block > 0x7FFFFF00ll) return ZB_ERR_UNSUPPORTED;
+    if (budget < 1 || budget > slots || static_cast<long long>(sinks) + recent > budget) return ZB_ERR_SHAPE;
+    if (!table || !mass || !lens || !table_out || !lens_out) return ZB_ERR_NULL;
+    if (table == table_out) return ZB_ERR_SHAPE;
+    for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(mass),
+                          static_cast<const void*>(lens), static_cast<const void*>(table_out),
+                          static_cast<const void*>(lens_out), static_cast<const void*>(kept)})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return ZB_ERR_ALIGN;
+    DeviceInfo dev;
+    zb_status e = current_device(&dev);
+    if (e != ZB_OK) return e;
+    kv8::EvictArgs a{table, mass, lens, slots, block, budget, sinks, recent, table_out, lens_out, kept,
+                     slots <= kv8::E_KEYS, dev.status};
+    const int smem = a.keys_in_smem ? slots * 4 : 0;
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(kv8::evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kv8::E_KEYS * 4) !=
+        cudaSuccess)
+        return ZB_ERR_CUDA;
+    kv8::evict_kernel<<<heads, kv8::E_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}

@@ -159,5 +159,6 @@ def evict_blocks(table, mass, length, block, budget, sinks, recent):
         return list(table), length, list(range(nb))
     middle = sorted(range(sinks, nb - recent), key=lambda b: (-mass[table[b]], b))
     kept = sorted(list(range(sinks)) + middle[:budget - sinks - recent] + list(range(nb - recent, nb)))
-    gone = [b for b in range(nb) if b not in set(kept)]
+    stay = set(kept)
+    gone = [b for b in range(nb) if b not in stay]
     return ([table[b] for b in kept] + [table[b] for b in gone] + list(table[nb:]), length - block * len(gone), kept)
