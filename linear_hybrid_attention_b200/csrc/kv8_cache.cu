@@ -13,7 +13,7 @@
 //
 // Rounding is decided exactly.  x / s in fp32 may land on a tie that the exact
 // quotient misses by less than its rounding; where the quotient is that near a
-// tie (one value in some ten thousand), the sign of the fused x - (k + 1/2) s,
+// tie (one value in some thousands), the sign of the fused x - (k + 1/2) s,
 // which no rounding can change, decides.
 #include <cuda_runtime.h>
 
@@ -34,32 +34,32 @@ ZB_DEVINL float exact_round(float x, float s, float t) {
     return k + ((r > 0.f || (r == 0.f && odd)) ? 1.f : 0.f);
 }
 
-ZB_DEVINL float quotient(float x, float s, float inv) {
-    // 1 / s overflows for a scale that is itself subnormal or nearly so
-    return s < 0x1p-120f ? x / s : x * inv;
-}
+constexpr float TINY_SCALE = 0x1p-120f;   // 1 / s overflows below about 2^-128
 
-ZB_DEVINL int code_int8(float x, float s, float inv) {
-    const float t = quotient(x, s, inv);
-    float q = rintf(t);
-    if (fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = exact_round(x, s, t);
-    q = fminf(fmaxf(q, -127.f), 127.f);
-    return static_cast<int>(q);
-}
-
-// The value of the e4m3 code nearest to x / s.
-ZB_DEVINL float value_e4m3(float x, float s, float inv) {
-    const float t = quotient(x, s, inv);
-    const uint32_t bits = __float_as_uint(t) & 0x7FFFFFFFu;
-    const int off = static_cast<int>(bits & 0xFFFFFu) - 0x80000;
-    // off the grid's ties by more than the quotient's error: the conversion is exact
-    if (bits >= 0x3C800000u && (off > 256 || off < -256)) return t;
-    if (bits == 0u) return t;
-    int e = static_cast<int>(bits >> 23) - 127;
-    if (e < -6) e = -6;
-    const float step = __uint_as_float(static_cast<uint32_t>(e - 3 + 127) << 23);
-    const float q = exact_round(fabsf(x), s * step, fabsf(t) / step);
-    return copysignf(fminf(q * step, 448.f), t);
+// Eight codes of x for a scale of at least TINY_SCALE.  Adding 1.5 * 2^23 rounds a
+// quotient to a whole number (ties to even) whose low byte is the code: half the
+// price of a conversion.  A value within 2^-13 of a tie sends the eight through
+// exact_round.
+ZB_DEVINL uint2 codes_int8(const float* x, float s, float inv) {
+    uint32_t u[8];
+    float far = 0.f;
+    const uint64_t inv2 = f2_pack(inv, inv), big2 = f2_pack(12582912.f, 12582912.f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t t = f2_mul(f2_pack(x[i], x[i + 1]), inv2), m = f2_add(t, big2);
+        float a, b, ma, mb;
+        f2_unpack(f2_sub(t, f2_sub(m, big2)), a, b);
+        f2_unpack(m, ma, mb);
+        far = fmax3(far, fabsf(a), fabsf(b));
+        u[i] = __float_as_uint(ma);
+        u[i + 1] = __float_as_uint(mb);
+    }
+    if (far > 0.5f - 0x1p-13f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(exact_round(x[i], s, x[i] * inv) + 12582912.f);
+    }
+    return make_uint2(prmt(prmt(u[0], u[1], 0x0040u), prmt(u[2], u[3], 0x0040u), 0x5410u),
+                      prmt(prmt(u[4], u[5], 0x0040u), prmt(u[6], u[7], 0x0040u), 0x5410u));
 }
 
 ZB_DEVINL uint32_t pack_e4m3x2(float lo, float hi) {
@@ -68,17 +68,50 @@ ZB_DEVINL uint32_t pack_e4m3x2(float lo, float hi) {
     return r;
 }
 
-template <int FMT>
-ZB_DEVINL uint2 codes8(const float* x, float s, float inv) {
-    uint32_t w[2] = {0u, 0u};
-    if (FMT == ZB_KV8_INT8) {
+// The value of the e4m3 code nearest to x / s, t its quotient in fp32.
+ZB_DEVINL float value_e4m3(float x, float s, float t) {
+    int e = static_cast<int>((__float_as_uint(t) >> 23) & 255u) - 127;
+    if (e < -6) e = -6;
+    const float step = __uint_as_float(static_cast<uint32_t>(e - 3 + 127) << 23);
+    const float q = exact_round(fabsf(x), s * step, fabsf(t) / step);
+    return copysignf(fminf(q * step, 448.f), t);
+}
+
+// The conversion instruction rounds t correctly, and t is the quotient to some
+// steps of fp32: only a value that near a tie between two codes (the 20 bits below
+// the code's mantissa), or below the normal codes, needs the exact form.
+ZB_DEVINL uint2 codes_e4m3(const float* x, float s, float inv) {
+    float t[8];
+    bool hard = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        t[i] = x[i] * inv;
+        const uint32_t b = __float_as_uint(t[i]) & 0x7FFFFFFFu;
+        hard |= ((b + 0x100u) & 0xFFFFFu) - 0x80000u <= 0x200u;
+        hard |= b - 1u < 0x3C800000u - 1u;
+    }
+    if (hard) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            w[i >> 2] |= (static_cast<uint32_t>(code_int8(x[i], s, inv)) & 0xFFu) << (8 * (i & 3));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-            w[i >> 2] |= pack_e4m3x2(value_e4m3(x[i], s, inv), value_e4m3(x[i + 1], s, inv)) << (8 * (i & 2));
+            if (t[i] != 0.f) t[i] = value_e4m3(x[i], s, t[i]);
+    }
+    return make_uint2(pack_e4m3x2(t[0], t[1]) | pack_e4m3x2(t[2], t[3]) << 16,
+                      pack_e4m3x2(t[4], t[5]) | pack_e4m3x2(t[6], t[7]) << 16);
+}
+
+template <int FMT>
+ZB_DEVINL uint2 codes8(const float* x, float s, float inv) {
+    if (s >= TINY_SCALE) return FMT == ZB_KV8_INT8 ? codes_int8(x, s, inv) : codes_e4m3(x, s, inv);
+    // a scale that is subnormal or nearly so: divide, and hold the result to the format
+    uint32_t w[2] = {0u, 0u};
+    for (int i = 0; i < 8; ++i) {
+        const float t = x[i] / s;
+        uint32_t c;
+        if (FMT == ZB_KV8_INT8)
+            c = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(exact_round(x[i], s, t), -127.f), 127.f))) & 0xFFu;
+        else
+            c = pack_e4m3x2(t != 0.f ? value_e4m3(x[i], s, t) : t, 0.f) & 0xFFu;
+        w[i >> 2] |= c << (8 * (i & 3));
     }
     return make_uint2(w[0], w[1]);
 }
@@ -96,7 +129,7 @@ struct AppendArgs {
 // HBM stream (256 B a token in, 128 B out): each thread has its eight 16-byte
 // loads in flight, a warp takes 16 rows, so a block is a whole number of warps.
 template <int FMT>
-__global__ void __launch_bounds__(A_THREADS) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(A_THREADS, 4) append_kernel(const AppendArgs a) {
     const int h = blockIdx.y, unit = blockIdx.x;
     const zb_kv8& c = a.c;
     const int B = c.block;
@@ -117,38 +150,44 @@ __global__ void __launch_bounds__(A_THREADS) append_kernel(const AppendArgs a) {
     const long long row0 = static_cast<long long>(unit) * UNIT + warp * 16;
     const long long blk = row0 / B;            // of this warp
     const bool live = blk < blocks;
-    const int chunk = lane & 7;
     uint4* tail[2] = {reinterpret_cast<uint4*>(c.k_tail) + static_cast<long long>(h) * B * 8,
                       reinterpret_cast<uint4*>(c.v_tail) + static_cast<long long>(h) * B * 8};
     const uint4* src[2] = {a.K + static_cast<long long>(h) * a.n * 8, a.V + static_cast<long long>(h) * a.n * 8};
+    // the warp's 16 rows: those before `old` come from the tail, those before `all` exist
+    const int old = static_cast<int>(min(max(held - row0, 0ll), 16ll));
+    const int all = static_cast<int>(min(max(rows - row0, 0ll), 16ll));
     uint4 x[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+        const uint4* in = src[t] + (row0 - held) * 8 + lane;   // row lane / 8, piece lane % 8
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const long long r = row0 + i * 4 + (lane >> 3);
+            const int r = i * 4 + (lane >> 3);
             x[t][i] = make_uint4(0, 0, 0, 0);
-            if (r < held) x[t][i] = tail[t][r * 8 + chunk];
-            else if (r < rows) x[t][i] = __ldg(src[t] + (r - held) * 8 + chunk);
+            if (r >= old && r < all) x[t][i] = __ldg(in + i * 32);
+        }
+        if (old > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i * 4 + (lane >> 3) < old) x[t][i] = tail[t][row0 * 8 + i * 32 + lane];
         }
     }
     // the block's largest magnitude: as integers, so that NaN is above infinity
+    const int slot = live ? slot_of(c, h, first + blk, a.status) : 0;
     __shared__ uint32_t top[2][A_THREADS / 32];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = max(m, max((w[j] & 0x7FFFu) << 16, w[j] & 0x7FFF0000u));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[t][i].x & 0x7FFF7FFFu, x[t][i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(x[t][i].z & 0x7FFF7FFFu, x[t][i].w & 0x7FFF7FFFu)));
         }
-        m = __reduce_max_sync(0xffffffffu, m);
+        m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0x7FFF0000u));
         if (lane == 0) top[t][warp] = m;
     }
     __syncthreads();
     if (live) {
-        const int slot = slot_of(c, h, first + blk, a.status);
         const long long at = static_cast<long long>(h) * c.slots + slot;
         const int w0 = warp & ~(B / 16 - 1);
 #pragma unroll
@@ -160,7 +199,7 @@ __global__ void __launch_bounds__(A_THREADS) append_kernel(const AppendArgs a) {
                                    : __uint_as_float(0x7FC00000u);
             const bool codes = finite && s > 0.f;
             const float inv = codes ? 1.f / s : 0.f;
-            uint2* out = reinterpret_cast<uint2*>(t ? c.v : c.k) + at * B * 8;
+            uint2* out = reinterpret_cast<uint2*>(t ? c.v : c.k) + (at * B + row0 - blk * B) * 8 + lane;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float f[8];
@@ -170,8 +209,7 @@ __global__ void __launch_bounds__(A_THREADS) append_kernel(const AppendArgs a) {
                     f[2 * j] = bf16_lo(w[j]);
                     f[2 * j + 1] = bf16_hi(w[j]);
                 }
-                const long long r = row0 + i * 4 + (lane >> 3) - blk * B;
-                out[r * 8 + chunk] = codes ? codes8<FMT>(f, s, inv) : make_uint2(0, 0);
+                out[i * 32] = codes ? codes8<FMT>(f, s, inv) : make_uint2(0, 0);
             }
             if (warp == w0 && lane == 0) (t ? c.v_scale : c.k_scale)[at] = s;
         }
@@ -206,39 +244,58 @@ __global__ void advance_kernel(const int32_t* lens, int32_t* out, int heads, int
 // ------------------------------------------------------------------ read ----
 // The newest n tokens of every head as bf16 (code * scale in fp32, rounded once);
 // rows before a head's first token are zeros.  An HBM stream: 64 B of codes in,
-// 128 B out a row; a thread moves 8 values of one tensor.
+// 128 B out a row.  A thread moves 8 values of one tensor in each of R_ROWS rows
+// that lie R_STEP apart, the table's entries of all of them read before any code; a
+// warp's stores are whole rows.
+constexpr int R_ROWS = 4, R_STEP = 32;
 template <int FMT>
 __global__ void __launch_bounds__(256) read_kernel(const zb_kv8 c, const int32_t* lens, int n, uint4* Ko, uint4* Vo,
                                                    int* status) {
     const int h = blockIdx.y;
     const long long cap = static_cast<long long>(c.slots) * c.block;
     const long long len = head_len(lens, h, cap);
-    const uint8_t* codes = blockIdx.z ? c.v : c.k;
+    const uint2* codes = reinterpret_cast<const uint2*>(blockIdx.z ? c.v : c.k);
     const float* scale = blockIdx.z ? c.v_scale : c.k_scale;
     uint4* out = (blockIdx.z ? Vo : Ko) + static_cast<long long>(h) * n * 8;
-    const int shift = 31 - __clz(c.block);
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < static_cast<long long>(n) * 8;
-         i += static_cast<long long>(gridDim.x) * 256) {
-        const long long tok = len - n + (i >> 3);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (tok >= 0) {
-            const int slot = slot_of(c, h, tok >> shift, status);
-            const long long at = static_cast<long long>(h) * c.slots + slot;
-            const float s = __ldg(scale + at);
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + (at * c.block + (tok & (c.block - 1))) * HD) +
-                                  (i & 7));
-            uint32_t p[4];
-            unpack4<FMT>(w.x, p[0], p[1]);
-            unpack4<FMT>(w.y, p[2], p[3]);
+    const int shift = 31 - __clz(c.block), q = threadIdx.x & 7;
+    for (long long base = static_cast<long long>(blockIdx.x) * R_STEP * R_ROWS; base < n;
+         base += static_cast<long long>(gridDim.x) * R_STEP * R_ROWS) {
+        long long at[R_ROWS], row[R_ROWS];
+        bool on[R_ROWS];
+#pragma unroll
+        for (int i = 0; i < R_ROWS; ++i) {
+            row[i] = base + i * R_STEP + (threadIdx.x >> 3);
+            const long long tok = len - n + row[i];
+            on[i] = row[i] < n && tok >= 0;
+            at[i] = on[i] ? static_cast<long long>(h) * c.slots + slot_of(c, h, tok >> shift, status) : 0;
+        }
+        uint2 w[R_ROWS];
+        float s[R_ROWS];
+#pragma unroll
+        for (int i = 0; i < R_ROWS; ++i) {
+            w[i] = make_uint2(0, 0);
+            s[i] = 0.f;
+            if (on[i]) {
+                const long long tok = len - n + row[i];
+                w[i] = __ldcs(codes + (at[i] * c.block + (tok & (c.block - 1))) * 8 + q);
+                s[i] = __ldg(scale + at[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R_ROWS; ++i) {
+            if (row[i] >= n) continue;
+            const uint32_t ww[2] = {w[i].x, w[i].y};
             uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = half2_floats(p[j]);
-                o[j] = pack_bf16x2(f.x * s, f.y * s);
+            for (int j = 0; j < 2; ++j) {
+                uint32_t p0, p1;
+                unpack4<FMT>(ww[j], p0, p1);
+                const float2 f0 = half2_floats(p0), f1 = half2_floats(p1);
+                o[2 * j] = pack_bf16x2(f0.x * s[i], f0.y * s[i]);
+                o[2 * j + 1] = pack_bf16x2(f1.x * s[i], f1.y * s[i]);
             }
-            v = make_uint4(o[0], o[1], o[2], o[3]);
+            out[row[i] * 8 + q] = on[i] ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
         }
-        __stcs(out + i, v);
     }
 }
 
@@ -444,7 +501,7 @@ extern "C" zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, u
     if (!aligned16(K) || !aligned16(V) || (reinterpret_cast<uintptr_t>(lens) & 3u)) return ZB_ERR_ALIGN;
     DeviceInfo dev;
     if ((e = current_device(&dev)) != ZB_OK) return e;
-    long long gx = (n * 8 + 255) / 256;
+    long long gx = (n + kv8::R_STEP * kv8::R_ROWS - 1) / (kv8::R_STEP * kv8::R_ROWS);
     if (gx > 65536) gx = 65536;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cache.heads), 2);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

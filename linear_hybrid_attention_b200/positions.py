@@ -107,7 +107,7 @@ def zb_rope(X, pos, turns, axes: int = 1, layout: str = "half", magnitude: float
     any non-overlapping view of X's shape, X itself among them; contiguous if not given."""
     b, h, n, xs = _view(X, "X")
     if out is None:
-        out = torch.empty(X.shape, dtype=torch.bfloat16, device=X.device)
+        out = torch.empty_like(X, memory_format=torch.contiguous_format)
     elif out.shape != X.shape or out.device != X.device:
         raise ValueError(f"out must have X's shape and device, got {tuple(out.shape)} on {out.device}")
     if turns is None:
@@ -145,7 +145,7 @@ def _rows_out(like, out: Optional[torch.Tensor], name: str, contiguous: bool):
     if like is None:
         return None
     if out is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     _view(out, name)
     if out.shape != like.shape or out.device != like.device or (contiguous and not out.is_contiguous()):
         raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}bf16 {tuple(like.shape)} tensor on "
