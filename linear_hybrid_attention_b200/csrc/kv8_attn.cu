@@ -7,13 +7,15 @@
 //
 // Bound by the cache's bytes (128 a token): every byte is read once.  Work is cut
 // into chunks of 64 keys, laid end to end over all heads (and 16-row tiles of
-// their queries), and each CTA takes an equal run of chunks, whatever the heads'
-// lengths; lengths are read on the device, so a captured graph serves all of them.
-// Each of the 8 warps of a CTA streams chunks of its own through a ring of
-// STAGES bulk copies (4 KB of keys, 4 KB of values each): no barrier is shared
-// between warps but at the end of a head's run, where the CTA joins their partial
-// sums.  A run that is not the whole of a head goes to the workspace, and the join
-// kernel adds the runs up.
+// their queries); each warp takes an equal run of chunks, whatever the heads'
+// lengths, the 12 warps of a CTA neighbouring ones.  Lengths are read on the
+// device, so a captured graph serves all of them.  A warp streams its chunks
+// through a ring of its own of STAGES bulk copies (4 KB of keys, 4 KB of values
+// each) across the heads it meets, and writes what lies wholly in its run at once:
+// the warps meet only at the end, where the CTA joins the parts of heads that
+// several of them hold.  (Joining at every head's end instead cost a batch with
+// some one-token sequences 3 us for each of them.)  What several CTAs hold goes to
+// the workspace, and the join kernel adds it up.
 //
 // The codes go to the matrix instruction as fp16, which holds both formats
 // exactly; the scales stay in fp32 (s_k multiplies the logits, s_v the chunk's
@@ -22,13 +24,18 @@
 // and its 8 bytes of four values in one piece each.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace zb {
 namespace kv8 {
 
-constexpr int WARPS = 8;
-constexpr int STAGES = 3;
+// Twelve warps of two stages, not eight of three: the ring holds as much (192 KB),
+// and three warps a scheduler hide what two leave open (256 views, one token:
+// 145 -> %s us).
+constexpr int WARPS = 12;
+constexpr int STAGES = 2;
 constexpr int TILE = 16;                         // query rows of an item
 constexpr uint32_t HALF_STAGE = CHUNK * HD;      // 4 KB of codes
 
@@ -41,9 +48,10 @@ struct AttnArgs {
     int rows, n_q, tiles;        // query rows a head (its group's heads x n_q), items a head
     int causal;
     float scale_log2;
+    long long runs;              // partial results of CTAs; those of single warps follow
     int groups;                  // weight sums a head: runs of min(block, 64) keys, or 0
     // workspace
-    float* part_o;               // [slots of partial runs][TILE][64]
+    float* part_o;               // [runs, then one a warp][TILE][64]
     float2* part_ml;             // [...][TILE]: running maximum (log2 units) and sum
     int2* item;                  // [heads * tiles]: first partial run, number of runs
     float* gsum;                 // [heads][groups][rows]: log2 of a row's sum over a group
@@ -52,22 +60,30 @@ struct AttnArgs {
     unsigned long long timeout_ns;
 };
 
+// A warp's part of an item that others hold parts of too (item -1: none).  Entry 2 w
+// is the part that warp w's run starts with, in its row of part_o; entry 2 w + 1 the
+// part it ends with, in its ring.
+struct Piece {
+    long long item;
+    int from_start, to_end;      // it begins / ends the item
+};
+
 struct __align__(128) AttnSmem {
     uint8_t ring[WARPS][STAGES][2][HALF_STAGE];
-    float o[WARPS][TILE][HD];
-    float m[WARPS][TILE], l[WARPS][TILE];
+    float m[2 * WARPS][TILE], l[2 * WARPS][TILE];
+    Piece piece[2 * WARPS];
     uint64_t full[WARPS][STAGES];
     unsigned long long wsum[WARPS];
-    long long total, start_before;
+    long long start_before;
     int start_head;
     int abort_flag;
 };
 
-// Where a warp stands in the CTA's run [at, end): the current item and the chunks
-// of it that fall into the run.
+// Where a warp stands in its run: the current item and the chunks of it that fall
+// into the run.
 struct Cursor {
     int h, tile;
-    int c, c1;            // next chunk of this warp, end of the item's part
+    int c, c1;            // next chunk, end of the item's part
     int c0;               // first chunk of the item's part
     int nc;               // chunks of the item
     long long left;       // chunks of the run after this part
@@ -136,7 +152,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         k.c0 = static_cast<int>(into - static_cast<long long>(k.tile) * k.nc);
         const long long here = min(left, static_cast<long long>(k.nc - k.c0));
         k.c1 = k.c0 + static_cast<int>(here);
-        k.c = k.c0 + warp;
+        k.c = k.c0;
         k.left = left - here;
     };
     auto next_part = [&](Cursor& k) -> bool {       // the run's next item
@@ -149,14 +165,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         open(k, h, static_cast<long long>(t) * chunks_of(head_len(a.lens, h, cap)), k.left);
         return true;
     };
+    // this warp's run within the CTA's, and the head it starts in
+    const long long wa = at + (end - at) * warp / WARPS, wb = at + (end - at) * (warp + 1) / WARPS;
+    if (lane < 2) sm.piece[2 * warp + lane].item = -1;
     Cursor cur, iss;
-    open(cur, sm.start_head, at - sm.start_before, end - at);
-    iss = cur;
-    bool more = true;                                // the issue cursor stands on a part
-    auto settle = [&]() {                            // move the issue cursor to this warp's next chunk
-        while (more && iss.c >= iss.c1) more = next_part(iss);
+    bool running = wa < wb;
+    if (running) {
+        int h = sm.start_head;
+        long long b = sm.start_before;
+        for (;; ++h) {
+            const long long n = static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+            if (wa < b + n) break;
+            b += n;
+        }
+        open(cur, h, wa - b, wb - wa);
+        iss = cur;
+    }
+    bool more = running;                             // the issue cursor stands on a chunk
+    auto settle = [&]() {
+        if (iss.c >= iss.c1) more = next_part(iss);
     };
-    settle();
 
     const WaitCtx wc{a.status, &sm.abort_flag, a.timeout_ns};
     uint8_t(*ring)[2][HALF_STAGE] = sm.ring[warp];
@@ -164,7 +192,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     float ks_q[STAGES], vs_q[STAGES];                // scales of the chunks in the ring (lane: piece)
     for (int s = 0; s < STAGES; ++s) ks_q[s] = vs_q[s] = 0.f;
     float ks_new = 0.f, vs_new = 0.f;
+    int entry = 0;                                   // table entry of the lane's piece of the next chunk to issue
     bool dead = false;
+    auto fetch = [&]() {
+        if (!more) return;
+        const long long key = static_cast<long long>(iss.c) * CHUNK + lane * PIECE_ROWS;
+        if (lane < PIECES && key < head_len(a.lens, iss.h, cap))
+            entry = __ldg(c.table + static_cast<long long>(iss.h) * c.slots + (key >> shift));
+    };
+    fetch();
 
     // Start the copies of the issue cursor's chunk; its scales land in ks_new, vs_new.
     auto issue = [&]() {
@@ -178,7 +214,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         __syncwarp();
         if (lane < have) {
             const long long key = key0 + lane * PIECE_ROWS;
-            const int slot = slot_of(c, iss.h, key >> shift, a.status);
+            int slot = entry;
+            if (slot < 0 || slot >= c.slots) {       // as slot_of
+                flag_status(a.status, ZB_ERR_INDEX);
+                slot = 0;
+            }
             const long long blk = static_cast<long long>(iss.h) * c.slots + slot;
             const long long byte = (blk * B + (key & (B - 1))) * HD;
             bulk_load(smem_addr(&ring[s][0][lane * PIECE_BYTES]), c.k + byte, PIECE_BYTES, bar);
@@ -187,8 +227,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             vs_new = __ldg(c.v_scale + blk);
         }
         ++issued;
-        iss.c += WARPS;
+        ++iss.c;
         settle();
+        fetch();
     };
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -199,7 +240,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         }
     }
 
-    bool running = true;
     while (running) {
         // ---- one item's part of the run ------------------------------------
         const long long len = head_len(a.lens, cur.h, cap);
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-        for (; cur.c < cur.c1; cur.c += WARPS) {
+        for (; cur.c < cur.c1; ++cur.c) {
             const int st = used % STAGES;
             if (!dead && !mbar_wait_warp(smem_addr(&sm.full[warp][st]), (used / STAGES) & 1, wc)) dead = true;
             if (dead) break;                         // nothing more is issued; drained below
@@ -274,13 +314,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             for (int nt = 0; nt < 8; ++nt) {
                 const int key = 16 * (nt >> 1) + 8 * (nt & 1) + 4 * (g & 1) + (g >> 1);
                 const uint4 w = *reinterpret_cast<const uint4*>(kc + key * HD + c4 * 16);
-                x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     uint32_t b0, b1;
                     unpack4<FMT>(ww[s], b0, b1);
-                    mma_f16(x[nt], qa[s], b0, b1);
+                    if (s == 0) mma_f16_new(x[nt], qa[s], b0, b1);
+                    else mma_f16(x[nt], qa[s], b0, b1);
                 }
             }
             // ---- softmax over the chunk ------------------------------------
@@ -352,18 +392,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 }
             }
             // ---- values: lane's output features are 8 g ... (columns) of tile j: feature 8 n + j
+            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {   // rare once the maxima settle
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                o[j][0] *= corr[0];
-                o[j][1] *= corr[0];
-                o[j][2] *= corr[1];
-                o[j][3] *= corr[1];
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2 * US; ++e) o[j][e] *= corr[e >> 1];
+                }
             }
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) {
                 float acc[8][4];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
                 for (int t = p * GK; t < (p + 1) * GK; ++t) {
                     uint2 w[4];                      // rows 16 t + 4 i + c4: keys (2t, 2 c4), (2t, 2 c4 + 1), (2t + 1, ...)
@@ -380,7 +418,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                         unpack4<FMT>(prmt(a2, a3, 0x5140u), b1[0], b1[1]);
                         unpack4<FMT>(prmt(a2, a3, 0x7362u), b1[2], b1[3]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) mma_f16(acc[i * 4 + q], pa[t], b0[q], b1[q]);
+                        for (int q = 0; q < 4; ++q) {
+                            if (t == p * GK) mma_f16_new(acc[i * 4 + q], pa[t], b0[q], b1[q]);
+                            else mma_f16(acc[i * 4 + q], pa[t], b0[q], b1[q]);
+                        }
                     }
                 }
                 const float vs = __shfl_sync(0xffffffffu, vsl, p);
@@ -388,10 +429,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 const float v0 = end0 > p * PIECE_ROWS ? vs : 0.f, v1 = end1 > p * PIECE_ROWS ? vs : 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    o[j][0] = fmaf(acc[j][0], v0, o[j][0]);
-                    o[j][1] = fmaf(acc[j][1], v0, o[j][1]);
-                    o[j][2] = fmaf(acc[j][2], v1, o[j][2]);
-                    o[j][3] = fmaf(acc[j][3], v1, o[j][3]);
+#pragma unroll
+                    for (int e = 0; e < 2 * US; ++e) o[j][e] = fmaf(acc[j][e], e < 2 ? v0 : v1, o[j][e]);
                 }
             }
             __syncwarp();                            // the stage has been read
@@ -407,70 +446,122 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             vs_q[STAGES - 1] = vs_new;
         }
 
-        // ---- join the warps' partial results of the part --------------------
+        // ---- the part's result ---------------------------------------------
+        constexpr int US = ROWS8 ? 1 : 2;
+        const long long it = static_cast<long long>(cur.h) * a.tiles + cur.tile;
+        const bool starts = cur.c0 == 0, ends = cur.c1 == cur.nc, last = cur.left == 0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < US; ++u) {
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-            const int r = g + 8 * u;
-            if (c4 == 0) {
-                sm.m[warp][r] = m[u];
-                sm.l[warp][r] = l[u];
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {            // features 16 c4 + 8 e + j
-                float4* d = reinterpret_cast<float4*>(&sm.o[warp][r][16 * c4 + 8 * e]);
-                d[0] = make_float4(o[0][2 * u + e], o[1][2 * u + e], o[2][2 * u + e], o[3][2 * u + e]);
-                d[1] = make_float4(o[4][2 * u + e], o[5][2 * u + e], o[6][2 * u + e], o[7][2 * u + e]);
-            }
         }
-        __syncthreads();
-        const long long it = static_cast<long long>(cur.h) * a.tiles + cur.tile;
-        const long long run = it + blockIdx.x;
-        const bool whole = cur.c0 == 0 && cur.c1 == cur.nc;
-        for (int i = threadIdx.x; i < live_rows * (HD / 4); i += WARPS * 32) {
-            const int r = i / (HD / 4), q = i % (HD / 4);
-            float M = -INFINITY;
+        if (starts && ends) {                        // nobody else's: write the outputs
+            const long long run = it + blockIdx.x;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.m[w][r]);
-            float L = 0.f;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float f = sm.m[w][r] == -INFINITY ? 0.f : ex2(sm.m[w][r] - M);
-                const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][r][4 * q]);
-                L = fmaf(sm.l[w][r], f, L);
-                s.x = fmaf(v.x, f, s.x);
-                s.y = fmaf(v.y, f, s.y);
-                s.z = fmaf(v.z, f, s.z);
-                s.w = fmaf(v.w, f, s.w);
-            }
-            if (q == 0) a.part_ml[run * TILE + r] = make_float2(M, L);
-            if (whole) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;   // no key: zeros; NaN stays
+            for (int u = 0; u < US; ++u) {
+                const int r = g + 8 * u;
+                if (r >= live_rows) continue;
                 const long long row = static_cast<long long>(cur.h) * a.rows + row0 + r;
-                reinterpret_cast<uint2*>(a.O + row * HD)[q] =
-                    make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
-                if (q == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M - P_SHIFT + log2f(L)) * LN2;
-            } else {
-                reinterpret_cast<float4*>(a.part_o + (run * TILE + r) * HD)[q] = s;
+                const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];   // no key: zeros; NaN stays
+                uint4* d = reinterpret_cast<uint4*>(a.O + row * HD) + 2 * c4;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {        // features 16 c4 + 8 e + j
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = pack_bf16x2(o[2 * j][2 * u + e] * inv, o[2 * j + 1][2 * u + e] * inv);
+                    d[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (c4 == 0) {
+                    if (a.lse) a.lse[row] = l[u] == 0.f ? -INFINITY : (m[u] - P_SHIFT + log2f(l[u])) * LN2;
+                    a.part_ml[run * TILE + r] = make_float2(m[u], l[u]);
+                }
             }
+            if (lane == 0) a.item[it] = make_int2(static_cast<int>(run), 1);
+        } else {
+            // the run goes on: to the warp's row of the workspace; else its ring, now idle, has room
+            const int e2 = 2 * warp + (last ? 1 : 0);
+            float* dst = last ? reinterpret_cast<float*>(&ring[0][0][0])
+                              : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + warp) * TILE * HD;
+            // (after a wait that gave up this may hold anything, and the status says so)
+#pragma unroll
+            for (int u = 0; u < US; ++u) {
+                const int r = g + 8 * u;
+                if (c4 == 0) {
+                    sm.m[e2][r] = m[u];
+                    sm.l[e2][r] = l[u];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float4* d = reinterpret_cast<float4*>(dst + r * HD + 16 * c4 + 8 * e);
+                    d[0] = make_float4(o[0][2 * u + e], o[1][2 * u + e], o[2][2 * u + e], o[3][2 * u + e]);
+                    d[1] = make_float4(o[4][2 * u + e], o[5][2 * u + e], o[6][2 * u + e], o[7][2 * u + e]);
+                }
+            }
+            if (lane == 0) sm.piece[e2] = Piece{it, starts, ends};
         }
-        if (threadIdx.x == 0 && cur.c0 == 0) {
-            // the runs of this item: CTAs from this one to the one with its last chunk
-            const long long last = (at + (end - at - cur.left) - cur.c1 + cur.nc) - 1;   // its place in all chunks
-            const long long to = ((last + 1) * ctas - 1) / total;
-            a.item[it] = make_int2(static_cast<int>(run), static_cast<int>(to - blockIdx.x + 1));
-        }
-        __syncthreads();                             // sm.o is free again
         running = next_part(cur);
     }
     // copies of a warp that gave up are still writing its ring
     for (; used < issued; ++used) {
-        const WaitCtx drain{a.status, &sm.abort_flag, drain_timeout_ns(a.timeout_ns)};
-        const uint64_t t0 = globaltimer_ns();
+        const uint64_t t0 = globaltimer_ns(), limit = drain_timeout_ns(a.timeout_ns);
         while (!mbar_try_wait(smem_addr(&sm.full[warp][used % STAGES]), (used / STAGES) & 1))
-            if (globaltimer_ns() - t0 > drain.timeout_ns) break;
+            if (globaltimer_ns() - t0 > limit) break;
+    }
+    __threadfence_block();
+    __syncthreads();
+    // ---- parts of one item that neighbouring warps hold ---------------------
+    for (int e0 = 0; e0 < 2 * WARPS;) {
+        const long long it = sm.piece[e0].item;
+        int e1 = e0 + 1, tail = e0;                  // entries of the item: [e0, e1), unused ones among them
+        if (it >= 0)
+            for (; e1 < 2 * WARPS && (sm.piece[e1].item == it || sm.piece[e1].item < 0); ++e1)
+                if (sm.piece[e1].item == it) tail = e1;
+        if (it >= 0) {
+            const int h = static_cast<int>(it / a.tiles), row0 = static_cast<int>(it % a.tiles) * TILE;
+            const int live_rows = min(TILE, a.rows - row0);
+            const long long run = it + blockIdx.x;
+            const bool whole = sm.piece[e0].from_start && sm.piece[tail].to_end;
+            for (int i = threadIdx.x; i < live_rows * (HD / 4); i += WARPS * 32) {
+                const int r = i / (HD / 4), q = i % (HD / 4);
+                float M = -INFINITY, L = 0.f;
+                for (int e = e0; e <= tail; ++e)
+                    if (sm.piece[e].item == it) M = fmaxf(M, sm.m[e][r]);
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int e = e0; e <= tail; ++e) {
+                    if (sm.piece[e].item != it) continue;
+                    const float f = sm.m[e][r] == -INFINITY ? 0.f : ex2(sm.m[e][r] - M);
+                    const float* src = (e & 1) ? reinterpret_cast<const float*>(&sm.ring[e >> 1][0][0][0])
+                                               : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + (e >> 1)) * TILE * HD;
+                    const float4 v = *reinterpret_cast<const float4*>(src + r * HD + 4 * q);
+                    L = fmaf(sm.l[e][r], f, L);
+                    s.x = fmaf(v.x, f, s.x);
+                    s.y = fmaf(v.y, f, s.y);
+                    s.z = fmaf(v.z, f, s.z);
+                    s.w = fmaf(v.w, f, s.w);
+                }
+                if (q == 0) a.part_ml[run * TILE + r] = make_float2(M, L);
+                if (whole) {
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    const long long row = static_cast<long long>(h) * a.rows + row0 + r;
+                    reinterpret_cast<uint2*>(a.O + row * HD)[q] =
+                        make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
+                    if (q == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M - P_SHIFT + log2f(L)) * LN2;
+                } else {
+                    reinterpret_cast<float4*>(a.part_o + (run * TILE + r) * HD)[q] = s;
+                }
+            }
+        }
+        e0 = e1;
+    }
+    // the runs of the items that begin in this one: from this CTA to the one with the last chunk
+    if (lane < 2 && sm.piece[2 * warp + lane].item >= 0 && sm.piece[2 * warp + lane].from_start) {
+        const Piece p = sm.piece[2 * warp + lane];
+        // a part that begins an item is the warp's last, and ends where its run ends
+        const long long len = head_len(a.lens, static_cast<int>(p.item / a.tiles), cap);
+        const long long final = wb - (cur.c1 - cur.c0) + chunks_of(len) - 1;
+        const long long to = ((final + 1) * ctas - 1) / total;
+        a.item[p.item] = make_int2(static_cast<int>(p.item + blockIdx.x), static_cast<int>(to - blockIdx.x + 1));
     }
 }
 
@@ -480,6 +571,46 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
 // parts): every part works out the rows' log-sum-exp again, part 0 writes the
 // outputs, and the blocks are shared out over the parts.
 constexpr int JOIN_ROWS = 32;
+
+// One row's runs added up, by the 16 threads (one half warp) that hold 4 of its
+// features each: each thread reads the maximum and sum of one run in sixteen, so a
+// row's runs cost two dependent reads, not two a run.
+template <int TR>
+ZB_DEVINL void add_runs(const AttnArgs& a, int2 it, int r, int q, bool outputs, float& M, float& L, float4& s) {
+    const uint32_t half = 0xFFFFu << (lane_id() & 16);
+    M = -INFINITY;
+    for (int i = q; i < it.y; i += 16) M = fmaxf(M, a.part_ml[static_cast<long long>(it.x + i) * TR + r].x);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+    L = 0.f;
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < it.y; i0 += 16) {
+        float f = 0.f, l = 0.f;
+        if (i0 + q < it.y) {
+            const float2 ml = a.part_ml[static_cast<long long>(it.x + i0 + q) * TR + r];
+            if (ml.y != 0.f) {
+                f = ex2(ml.x - M);
+                l = ml.y * f;
+            }
+        }
+        const int n = min(16, it.y - i0);
+        const float4* v = reinterpret_cast<const float4*>(a.part_o + (static_cast<long long>(it.x + i0) * TR + r) * HD) + q;
+        const bool read = outputs && it.y > 1;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            L += __shfl_sync(half, l, i, 16);
+            const float fi = __shfl_sync(half, f, i, 16);
+            if (read && fi != 0.f) {
+                const float4 w = v[static_cast<long long>(i) * TR * (HD / 4)];
+                s.x = fmaf(w.x, fi, s.x);
+                s.y = fmaf(w.y, fi, s.y);
+                s.z = fmaf(w.z, fi, s.z);
+                s.w = fmaf(w.w, fi, s.w);
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     __shared__ float lse2[JOIN_ROWS];
     const zb_kv8& c = a.c;
@@ -501,25 +632,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
         const int row = r0 + r;
         if (row < a.rows) {
             const int2 it = a.item[static_cast<long long>(h) * a.tiles + row / TILE];
-            const int rr = row % TILE;
-            float M = -INFINITY;
-            for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[static_cast<long long>(it.x + i) * TILE + rr].x);
-            float L = 0.f;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i = 0; i < it.y; ++i) {
-                const long long at = static_cast<long long>(it.x + i) * TILE + rr;
-                const float2 ml = a.part_ml[at];
-                if (ml.y == 0.f) continue;
-                const float f = ex2(ml.x - M);
-                L = fmaf(ml.y, f, L);
-                if (part == 0 && it.y > 1) {
-                    const float4 v = reinterpret_cast<const float4*>(a.part_o + at * HD)[q];
-                    s.x = fmaf(v.x, f, s.x);
-                    s.y = fmaf(v.y, f, s.y);
-                    s.z = fmaf(v.z, f, s.z);
-                    s.w = fmaf(v.w, f, s.w);
-                }
-            }
+            float M, L;
+            float4 s;
+            add_runs<TILE>(a, it, row % TILE, q, part == 0, M, L, s);
             const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
             if (q == 0) lse2[row] = t;
             if (part == 0 && it.y > 1) {
@@ -558,23 +673,9 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
     const int2 it = len ? a.item[blockIdx.x] : make_int2(0, 0);
     const int q = threadIdx.x & 15;
     for (int r = threadIdx.x >> 4; r < TR && tile * TR + r < a.rows; r += 16) {
-        float M = -INFINITY, L = 0.f;
-        for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[static_cast<long long>(it.x + i) * TR + r].x);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < it.y; ++i) {
-            const long long at = static_cast<long long>(it.x + i) * TR + r;
-            const float2 ml = a.part_ml[at];
-            if (ml.y == 0.f) continue;
-            const float f = ex2(ml.x - M);
-            L = fmaf(ml.y, f, L);
-            if (it.y > 1) {
-                const float4 v = reinterpret_cast<const float4*>(a.part_o + at * HD)[q];
-                s.x = fmaf(v.x, f, s.x);
-                s.y = fmaf(v.y, f, s.y);
-                s.z = fmaf(v.z, f, s.z);
-                s.w = fmaf(v.w, f, s.w);
-            }
-        }
+        float M, L;
+        float4 s;
+        add_runs<TR>(a, it, r, q, true, M, L, s);
         const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
         const long long row = static_cast<long long>(h) * a.rows + tile * TR + r;
         if (q == 0 && a.lse2) a.lse2[row] = t;
@@ -627,9 +728,9 @@ Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
     Plan p{};
     p.rows = static_cast<long long>(heads_q / c.heads) * n_q;
     p.tiles = (p.rows + TILE - 1) / TILE;
-    p.runs = p.tiles * c.heads + MAX_SMS;
+    p.runs = p.tiles * c.heads + MAX_SMS;           // an item and a CTA: their sum is its run
     p.groups = add_mass ? static_cast<long long>(c.slots) * (c.block > CHUNK ? c.block / CHUNK : 1) : 0;
-    p.o = up256(static_cast<size_t>(p.runs) * TILE * HD * sizeof(float));
+    p.o = up256(static_cast<size_t>(p.runs + MAX_SMS * WARPS) * TILE * HD * sizeof(float));
     p.ml = up256(static_cast<size_t>(p.runs) * TILE * sizeof(float2));
     p.item = up256(static_cast<size_t>(p.tiles) * c.heads * sizeof(int2));
     p.gsum = up256(static_cast<size_t>(p.groups) * c.heads * p.rows * sizeof(float));
@@ -641,8 +742,14 @@ Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
 template <int FMT, bool ROWS8, int GK>
 zb_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
     auto* fn = attn_kernel<FMT, ROWS8, GK>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnSmem)) != cudaSuccess)
-        return ZB_ERR_CUDA;
+    static std::atomic<unsigned long long> done{0};  // devices that have the attribute set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ZB_ERR_CUDA;
+    if (!(done.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttnSmem)) != cudaSuccess)
+            return ZB_ERR_CUDA;
+        done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     fn<<<ctas, WARPS * 32, sizeof(AttnSmem), st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
 }
@@ -699,6 +806,7 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
     a.tiles = static_cast<int>(p.tiles);
     a.causal = causal != 0;
     a.scale_log2 = scale * kv8::LOG2E;
+    a.runs = p.runs;
     a.groups = static_cast<int>(p.groups);
     a.part_o = reinterpret_cast<float*>(w);
     a.part_ml = reinterpret_cast<float2*>(w + p.o);
