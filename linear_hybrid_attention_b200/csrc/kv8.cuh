@@ -91,6 +91,13 @@ ZB_DEVINL void mma_f16_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Transpose of an 8 x 8 matrix of 16-bit values, a pair of a row in each lane.
+ZB_DEVINL uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // ------------------------------------------------------------ host side ----
 inline zb_status check_cache(const zb_kv8& c, bool codes) {
     if (c.heads < 1 || c.slots < 1) return ZB_ERR_SHAPE;

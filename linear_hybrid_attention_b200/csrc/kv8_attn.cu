@@ -19,7 +19,10 @@
 //
 // The codes go to the matrix instruction as fp16, which holds both formats
 // exactly; the scales stay in fp32 (s_k multiplies the logits, s_v the chunk's
-// product).  Queries are scaled by a power of two per row to fp16's range.  The
+// product).  Queries are scaled by a power of two per row to fp16's range.  Keys and
+// features are the instruction's 16 rows and queries its 8 columns (S^T = K Q^T,
+// O^T = V^T P^T, P^T by an 8 x 8 transpose between the two): 8 query rows then cost
+// half of what they do as half-empty rows, and a code is unpacked once for 16.  The
 // features and keys a lane holds are chosen so that it reads its 16 bytes of a key
 // and its 8 bytes of four values in one piece each.
 #include <cuda_runtime.h>
@@ -36,7 +39,7 @@ namespace kv8 {
 // 145 -> %s us).
 constexpr int WARPS = 12;
 constexpr int STAGES = 2;
-constexpr int TILE = 16;                         // query rows of an item
+constexpr int TILE = 16;                         // most query rows of an item (8 if there are no more)
 constexpr uint32_t HALF_STAGE = CHUNK * HD;      // 4 KB of codes
 
 struct AttnArgs {
@@ -51,8 +54,8 @@ struct AttnArgs {
     long long runs;              // partial results of CTAs; those of single warps follow
     int groups;                  // weight sums a head: runs of min(block, 64) keys, or 0
     // workspace
-    float* part_o;               // [runs, then one a warp][TILE][64]
-    float2* part_ml;             // [...][TILE]: running maximum (log2 units) and sum
+    float* part_o;               // [runs, then one a warp][tile][64]
+    float2* part_ml;             // [...][tile]: running maximum (log2 units) and sum
     int2* item;                  // [heads * tiles]: first partial run, number of runs
     float* gsum;                 // [heads][groups][rows]: log2 of a row's sum over a group
     float* lse2;                 // [heads][rows]: log2 of a row's whole sum (more than JOIN_ROWS rows)
@@ -86,15 +89,17 @@ struct Cursor {
     int c, c1;            // next chunk, end of the item's part
     int c0;               // first chunk of the item's part
     int nc;               // chunks of the item
+    long long len;        // tokens of the head
     long long left;       // chunks of the run after this part
 };
 
 ZB_DEVINL int chunks_of(long long len) { return static_cast<int>((len + CHUNK - 1) / CHUNK); }
 
-// ROWS8: the item has at most 8 rows, the other half of the tile is not computed.
-// GK: 16-key steps that share a value scale (block / 16, at most 4).
-template <int FMT, bool ROWS8, int GK>
+// NT: groups of 8 query rows an item has.  GK: 16-key steps that share a value
+// scale (block / 16, at most 4).
+template <int FMT, int NT, int GK>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
+    constexpr int TR = 8 * NT;
     extern __shared__ uint8_t smem_raw[];
     AttnSmem& sm = *reinterpret_cast<AttnSmem*>(smem_raw);
     const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c4 = lane & 3;
@@ -147,7 +152,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     auto open = [&](Cursor& k, int h, long long into, long long left) {
         // position `into` of head h's chunks, `left` chunks to go in the run
         k.h = h;
-        k.nc = chunks_of(head_len(a.lens, h, cap));
+        k.len = head_len(a.lens, h, cap);
+        k.nc = chunks_of(k.len);
         k.tile = static_cast<int>(into / k.nc);
         k.c0 = static_cast<int>(into - static_cast<long long>(k.tile) * k.nc);
         const long long here = min(left, static_cast<long long>(k.nc - k.c0));
@@ -197,16 +203,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     auto fetch = [&]() {
         if (!more) return;
         const long long key = static_cast<long long>(iss.c) * CHUNK + lane * PIECE_ROWS;
-        if (lane < PIECES && key < head_len(a.lens, iss.h, cap))
+        if (lane < PIECES && key < iss.len)
             entry = __ldg(c.table + static_cast<long long>(iss.h) * c.slots + (key >> shift));
     };
     fetch();
 
     // Start the copies of the issue cursor's chunk; its scales land in ks_new, vs_new.
     auto issue = [&]() {
-        const long long len = head_len(a.lens, iss.h, cap);
         const long long key0 = static_cast<long long>(iss.c) * CHUNK;
-        const int have = static_cast<int>((min(len - key0, static_cast<long long>(CHUNK)) + PIECE_ROWS - 1) / PIECE_ROWS);
+        const int have = static_cast<int>((min(iss.len - key0, static_cast<long long>(CHUNK)) + PIECE_ROWS - 1) / PIECE_ROWS);
         const int s = issued % STAGES;
         const uint32_t bar = smem_addr(&sm.full[warp][s]);
         ks_new = vs_new = 0.f;
@@ -242,50 +247,56 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
 
     while (running) {
         // ---- one item's part of the run ------------------------------------
-        const long long len = head_len(a.lens, cur.h, cap);
-        const int row0 = cur.tile * TILE, live_rows = min(TILE, a.rows - row0);
+        const long long len = cur.len;
+        const int row0 = cur.tile * TR, live_rows = min(TR, a.rows - row0);
         const uint16_t* Q = a.Q + (static_cast<long long>(cur.h) * a.rows + row0) * HD;
-        uint32_t qa[4][4];
-        float qf[2];
-        long long lim[2];                            // keys the thread's two rows see
+        uint32_t qb[NT][4][2];                       // row 8 n + g, features 16 c4 ..
+        float qf[NT][2];                             // of the lane's columns: rows 8 n + 2 c4 + e
+        long long lim[NT][2];                        // keys they see
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = g + 8 * u;
-            float f[16];
-            uint32_t top = 0;
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + g;
             uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (r < live_rows && !(ROWS8 && u)) {
+            if (r < live_rows) {
                 w[0] = __ldg(reinterpret_cast<const uint4*>(Q + r * HD) + c4 * 2);
                 w[1] = __ldg(reinterpret_cast<const uint4*>(Q + r * HD) + c4 * 2 + 1);
             }
             const uint32_t ww[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+            uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[2 * i] = bf16_lo(ww[i]);
-                f[2 * i + 1] = bf16_hi(ww[i]);
-                top = max(top, max((ww[i] & 0x7FFFu) << 16, ww[i] & 0x7FFF0000u));
-            }
+            for (int i = 0; i < 8; ++i) top = max(top, max((ww[i] & 0x7FFFu) << 16, ww[i] & 0x7FFF0000u));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // row largest to [2^14, 2^15): exact in fp16 down to 2^-28 of it, and to 2^-39 of it below
-            int e = static_cast<int>(top >> 23) - 127;
-            e = max(e, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+            const bool finite = top < 0x7F800000u;
+            const int e = max(static_cast<int>(top >> 23) - 127, -100);
+            const float up = finite ? __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23) : 0.f;
             // a row that is not finite has NaN logits throughout
-            qf[u] = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : down * a.scale_log2;
+            const float down = finite ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * a.scale_log2
+                                      : __uint_as_float(0x7FC00000u);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const float z = top >= 0x7F800000u ? 0.f : up;
-                qa[s][u] = pack_f16x2(f[4 * s] * z, f[4 * s + 1] * z);
-                qa[s][2 + u] = pack_f16x2(f[4 * s + 2] * z, f[4 * s + 3] * z);
-            }
-            lim[u] = a.causal ? len - a.n_q + 1 + (row0 + r) % a.n_q : len;
-        }
-        float o[8][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t v = ww[2 * s + i];
+                    qb[n][s][i] = finite ? pack_f16x2(bf16_lo(v) * up, bf16_hi(v) * up) : 0u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                qf[n][i] = __shfl_sync(0xffffffffu, down, (2 * c4 + i) * 4);
+                lim[n][i] = a.causal ? len - a.n_q + 1 + (row0 + 8 * n + 2 * c4 + i) % a.n_q : len;
+            }
+        }
+        float o[NT][4][4];                           // features 8 g + 2 j + (0, 0, 1, 1), rows 8 n + 2 c4 + (0, 1, 0, 1)
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
 
         for (; cur.c < cur.c1; ++cur.c) {
             const int st = used % STAGES;
@@ -297,10 +308,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             const uint8_t* kc = ring[st][0];
             uint8_t* vc = ring[st][1];
             // keys of the chunk that each row sees: all of them but at a head's end
-            const int end0 = static_cast<int>(max(min(lim[0] - key0, 64ll), 0ll));
-            const int end1 = static_cast<int>(max(min(lim[1] - key0, 64ll), 0ll));
+            int end[NT][2];
+            bool edge = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    end[n][i] = static_cast<int>(max(min(lim[n][i] - key0, 64ll), 0ll));
+                    edge |= end[n][i] < CHUNK;
+                }
+            }
+            edge = __any_sync(0xffffffffu, edge);
             const int valid = static_cast<int>(min(len - key0, 64ll));
-            const bool edge = __any_sync(0xffffffffu, end0 < CHUNK || end1 < CHUNK);
             if (valid < CHUNK) {
                 // rows behind the last token: what the ring held before could be any code
                 for (int i = valid * (HD / 8) + lane; i < CHUNK * HD / 8; i += 32)
@@ -308,129 +327,141 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 fence_proxy_async_smem();            // before a later copy into this stage
                 __syncwarp();
             }
-            // ---- logits: key (nt, n) of the instruction is row 16 (nt / 2) + 8 (nt & 1) + 4 (n & 1) + n / 2
-            float x[8][4];
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const int key = 16 * (nt >> 1) + 8 * (nt & 1) + 4 * (g & 1) + (g >> 1);
-                const uint4 w = *reinterpret_cast<const uint4*>(kc + key * HD + c4 * 16);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    uint32_t b0, b1;
-                    unpack4<FMT>(ww[s], b0, b1);
-                    if (s == 0) mma_f16_new(x[nt], qa[s], b0, b1);
-                    else mma_f16(x[nt], qa[s], b0, b1);
-                }
-            }
-            // ---- softmax over the chunk ------------------------------------
-            constexpr int US = ROWS8 ? 1 : 2;
-            float mx[2] = {m[0], m[1]};
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float ks = PIECES == 1 ? __shfl_sync(0xffffffffu, ksl, 0)
-                                             : __shfl_sync(0xffffffffu, ksl, (nt >> 1) / GK);
-#pragma unroll
-                for (int u = 0; u < US; ++u) {
-                    const float f = ks * qf[u];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = x[nt][2 * u + e] * f;
-                        if (edge) {                  // this lane's columns 2 c4 + e
-                            const int key = 16 * (nt >> 1) + 8 * (nt & 1) + 4 * e + c4;
-                            v = key < (u ? end1 : end0) ? v : -INFINITY;
-                        }
-                        x[nt][2 * u + e] = v;
-                        mx[u] = fmaxf(mx[u], v);
-                    }
-                }
-            }
-            float corr[2] = {1.f, 1.f}, ref[2];
-#pragma unroll
-            for (int u = 0; u < US; ++u) {
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-                ref[u] = mx[u] == -INFINITY ? 0.f : mx[u] - P_SHIFT;
-                corr[u] = m[u] == -INFINITY ? 0.f : ex2(m[u] - mx[u]);
-                m[u] = mx[u];
-                l[u] *= corr[u];
-            }
-            uint32_t pa[4][4];
+            // ---- logits: the instruction's row i of step t is key 16 t + 8 (i / 8) + 4 (i & 1) + i % 8 / 2
+            const int mine = 4 * (g & 1) + (g >> 1);
+            float x[NT][4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+                const uint4 w0 = *reinterpret_cast<const uint4*>(kc + (16 * t + mine) * HD + c4 * 16);
+                const uint4 w1 = *reinterpret_cast<const uint4*>(kc + (16 * t + 8 + mine) * HD + c4 * 16);
+                const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    pa[t][u] = pa[t][2 + u] = 0u;
-                    if (u < US) {
-                        const float p0 = ex2(x[2 * t][2 * u] - ref[u]), p1 = ex2(x[2 * t][2 * u + 1] - ref[u]);
-                        const float p2 = ex2(x[2 * t + 1][2 * u] - ref[u]), p3 = ex2(x[2 * t + 1][2 * u + 1] - ref[u]);
-                        pa[t][u] = pack_f16x2(p0, p1);
-                        pa[t][2 + u] = pack_f16x2(p2, p3);
-                        x[2 * t][2 * u] = (p0 + p1) + (p2 + p3);   // the step's sum, for l and the groups
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t ka[4];
+                    unpack4<FMT>(lo[s], ka[0], ka[2]);
+                    unpack4<FMT>(hi[s], ka[1], ka[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (s == 0) mma_f16_new(x[n][t], ka, qb[n][s][0], qb[n][s][1]);
+                        else mma_f16(x[n][t], ka, qb[n][s][0], qb[n][s][1]);
                     }
                 }
             }
+            // ---- softmax over the chunk: x[n][t][2 b + i] is key 16 t + 8 b + mine, row 8 n + 2 c4 + i
+            float ks[PIECES];
 #pragma unroll
-            for (int u = 0; u < US; ++u)
-                l[u] += (x[0][2 * u] + x[2][2 * u]) + (x[4][2 * u] + x[6][2 * u]);
-            if (a.groups) {
+            for (int p = 0; p < PIECES; ++p) ks[p] = __shfl_sync(0xffffffffu, ksl, p);
+            uint32_t pb[NT][4][2];
+            float corr[NT][2];
 #pragma unroll
-                for (int p = 0; p < PIECES; ++p) {
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                    for (int u = 0; u < US; ++u) {
-                        float s = 0.f;
+                for (int i = 0; i < 2; ++i) {
+                    float mx = m[n][i];
 #pragma unroll
-                        for (int t = p * GK; t < (p + 1) * GK; ++t) s += x[2 * t][2 * u];
-                        s += __shfl_xor_sync(0xffffffffu, s, 1);
-                        s += __shfl_xor_sync(0xffffffffu, s, 2);
-                        const int r = g + 8 * u;
-                        const long long grp = (key0 >> 6) * PIECES + p;
-                        if (c4 == 0 && r < live_rows && grp < a.groups)
-                            a.gsum[(static_cast<long long>(cur.h) * a.groups + grp) * a.rows + row0 + r] =
-                                log2f(s) + ref[u];
+                    for (int t = 0; t < 4; ++t) {
+                        const float f = ks[t / GK] * qf[n][i];
+                        x[n][t][i] *= f;
+                        x[n][t][2 + i] *= f;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            x[n][t][i] = 16 * t + mine < end[n][i] ? x[n][t][i] : -INFINITY;
+                            x[n][t][2 + i] = 16 * t + 8 + mine < end[n][i] ? x[n][t][2 + i] : -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) mx = fmax3(mx, x[n][t][i], x[n][t][2 + i]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float ref = mx == -INFINITY ? 0.f : mx - P_SHIFT;
+                    corr[n][i] = m[n][i] == -INFINITY ? 0.f : ex2(m[n][i] - mx);
+                    m[n][i] = mx;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        x[n][t][i] = ex2(x[n][t][i] - ref);
+                        x[n][t][2 + i] = ex2(x[n][t][2 + i] - ref);
+                    }
+                    float part[PIECES];              // the pieces' sums of this lane's keys
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        part[p] = 0.f;
+#pragma unroll
+                        for (int t = p * GK; t < (p + 1) * GK; ++t) part[p] += x[n][t][i] + x[n][t][2 + i];
+                    }
+                    float sum = 0.f;
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) sum += part[p];
+                    l[n][i] = fmaf(l[n][i], corr[n][i], sum);
+                    if (a.groups) {
+                        const int r = 8 * n + 2 * c4 + i;
+                        const long long grp0 = static_cast<long long>(cur.c) * PIECES;
+#pragma unroll
+                        for (int p = 0; p < PIECES; ++p) {
+                            float s = part[p];
+                            s += __shfl_xor_sync(0xffffffffu, s, 4);
+                            s += __shfl_xor_sync(0xffffffffu, s, 8);
+                            s += __shfl_xor_sync(0xffffffffu, s, 16);
+                            if (g == 0 && r < live_rows && grp0 + p < a.groups)
+                                a.gsum[(static_cast<long long>(cur.h) * a.groups + grp0 + p) * a.rows + row0 + r] =
+                                    __log2f(s) + ref;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    pb[n][t][0] = transpose8(pack_f16x2(x[n][t][0], x[n][t][1]));
+                    pb[n][t][1] = transpose8(pack_f16x2(x[n][t][2], x[n][t][3]));
+                }
+            }
+            bool moved = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) moved |= corr[n][0] != 1.f || corr[n][1] != 1.f;
+            if (__any_sync(0xffffffffu, moved)) {    // rare once the maxima settle
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][j][e] *= corr[n][e & 1];
                     }
                 }
             }
-            // ---- values: lane's output features are 8 g ... (columns) of tile j: feature 8 n + j
-            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {   // rare once the maxima settle
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2 * US; ++e) o[j][e] *= corr[e >> 1];
-                }
-            }
+            // ---- values: row i of the instruction's tile j is feature 8 (i % 8) + 2 j + i / 8 ----
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) {
-                float acc[8][4];
+                float acc[NT][4][4];
 #pragma unroll
                 for (int t = p * GK; t < (p + 1) * GK; ++t) {
-                    uint2 w[4];                      // rows 16 t + 4 i + c4: keys (2t, 2 c4), (2t, 2 c4 + 1), (2t + 1, ...)
+                    uint2 w[4];                      // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9 of the step
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         w[i] = *reinterpret_cast<const uint2*>(vc + (16 * t + 4 * i + c4) * HD + g * 8);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {    // four features at a time
-                        const uint32_t a0 = i ? w[0].y : w[0].x, a1 = i ? w[1].y : w[1].x;
-                        const uint32_t a2 = i ? w[2].y : w[2].x, a3 = i ? w[3].y : w[3].x;
-                        uint32_t b0[4], b1[4];
-                        unpack4<FMT>(prmt(a0, a1, 0x5140u), b0[0], b0[1]);
-                        unpack4<FMT>(prmt(a0, a1, 0x7362u), b0[2], b0[3]);
-                        unpack4<FMT>(prmt(a2, a3, 0x5140u), b1[0], b1[1]);
-                        unpack4<FMT>(prmt(a2, a3, 0x7362u), b1[2], b1[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                        uint32_t va[4];
+                        unpack4<FMT>(j < 2 ? prmt(w[0].x, w[1].x, sel) : prmt(w[0].y, w[1].y, sel), va[0], va[1]);
+                        unpack4<FMT>(j < 2 ? prmt(w[2].x, w[3].x, sel) : prmt(w[2].y, w[3].y, sel), va[2], va[3]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (t == p * GK) mma_f16_new(acc[i * 4 + q], pa[t], b0[q], b1[q]);
-                            else mma_f16(acc[i * 4 + q], pa[t], b0[q], b1[q]);
+                        for (int n = 0; n < NT; ++n) {
+                            if (t == p * GK) mma_f16_new(acc[n][j], va, pb[n][t][0], pb[n][t][1]);
+                            else mma_f16(acc[n][j], va, pb[n][t][0], pb[n][t][1]);
                         }
                     }
                 }
                 const float vs = __shfl_sync(0xffffffffu, vsl, p);
-                // a row that sees nothing of the piece takes nothing of it, whatever its scale is
-                const float v0 = end0 > p * PIECE_ROWS ? vs : 0.f, v1 = end1 > p * PIECE_ROWS ? vs : 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int n = 0; n < NT; ++n) {
+                    // a row that sees nothing of the piece takes nothing of it, whatever its scale is
+                    const float v[2] = {end[n][0] > p * PIECE_ROWS ? vs : 0.f, end[n][1] > p * PIECE_ROWS ? vs : 0.f};
 #pragma unroll
-                    for (int e = 0; e < 2 * US; ++e) o[j][e] = fmaf(acc[j][e], e < 2 ? v0 : v1, o[j][e]);
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][j][e] = fmaf(acc[n][j][e], v[e & 1], o[n][j][e]);
+                    }
                 }
             }
             __syncwarp();                            // the stage has been read
@@ -447,58 +478,52 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         }
 
         // ---- the part's result ---------------------------------------------
-        constexpr int US = ROWS8 ? 1 : 2;
         const long long it = static_cast<long long>(cur.h) * a.tiles + cur.tile;
         const bool starts = cur.c0 == 0, ends = cur.c1 == cur.nc, last = cur.left == 0;
+        const bool whole = starts && ends;           // nobody else's: the outputs themselves
+        const long long run = it + blockIdx.x;
+        // else the run goes on: to the warp's row of the workspace; or its ring, now idle, has room
+        // (after a wait that gave up this may hold anything, and the status says so)
+        const int e2 = 2 * warp + (last ? 1 : 0);
+        float* dst = last ? reinterpret_cast<float*>(&ring[0][0][0])
+                          : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + warp) * TR * HD;
 #pragma unroll
-        for (int u = 0; u < US; ++u) {
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float L = l[n][i];
+                L += __shfl_xor_sync(0xffffffffu, L, 4);
+                L += __shfl_xor_sync(0xffffffffu, L, 8);
+                L += __shfl_xor_sync(0xffffffffu, L, 16);
+                const float M = m[n][i];
+                const int r = 8 * n + 2 * c4 + i;
+                if (whole) {
+                    if (r < live_rows) {
+                        const long long row = static_cast<long long>(cur.h) * a.rows + row0 + r;
+                        const float inv = L == 0.f ? 0.f : 1.f / L;      // no key: zeros; NaN stays
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(o[n][j][i] * inv, o[n][j][2 + i] * inv);
+                        reinterpret_cast<uint4*>(a.O + row * HD)[g] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (g == 0) {
+                            if (a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M - P_SHIFT + log2f(L)) * LN2;
+                            a.part_ml[run * TR + r] = make_float2(M, L);
+                        }
+                    }
+                } else {
+                    if (g == 0) {
+                        sm.m[e2][r] = M;
+                        sm.l[e2][r] = L;
+                    }
+                    float4* d = reinterpret_cast<float4*>(dst + r * HD + 8 * g);
+                    d[0] = make_float4(o[n][0][i], o[n][0][2 + i], o[n][1][i], o[n][1][2 + i]);
+                    d[1] = make_float4(o[n][2][i], o[n][2][2 + i], o[n][3][i], o[n][3][2 + i]);
+                }
+            }
         }
-        if (starts && ends) {                        // nobody else's: write the outputs
-            const long long run = it + blockIdx.x;
-#pragma unroll
-            for (int u = 0; u < US; ++u) {
-                const int r = g + 8 * u;
-                if (r >= live_rows) continue;
-                const long long row = static_cast<long long>(cur.h) * a.rows + row0 + r;
-                const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];   // no key: zeros; NaN stays
-                uint4* d = reinterpret_cast<uint4*>(a.O + row * HD) + 2 * c4;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {        // features 16 c4 + 8 e + j
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = pack_bf16x2(o[2 * j][2 * u + e] * inv, o[2 * j + 1][2 * u + e] * inv);
-                    d[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                if (c4 == 0) {
-                    if (a.lse) a.lse[row] = l[u] == 0.f ? -INFINITY : (m[u] - P_SHIFT + log2f(l[u])) * LN2;
-                    a.part_ml[run * TILE + r] = make_float2(m[u], l[u]);
-                }
-            }
-            if (lane == 0) a.item[it] = make_int2(static_cast<int>(run), 1);
-        } else {
-            // the run goes on: to the warp's row of the workspace; else its ring, now idle, has room
-            const int e2 = 2 * warp + (last ? 1 : 0);
-            float* dst = last ? reinterpret_cast<float*>(&ring[0][0][0])
-                              : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + warp) * TILE * HD;
-            // (after a wait that gave up this may hold anything, and the status says so)
-#pragma unroll
-            for (int u = 0; u < US; ++u) {
-                const int r = g + 8 * u;
-                if (c4 == 0) {
-                    sm.m[e2][r] = m[u];
-                    sm.l[e2][r] = l[u];
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float4* d = reinterpret_cast<float4*>(dst + r * HD + 16 * c4 + 8 * e);
-                    d[0] = make_float4(o[0][2 * u + e], o[1][2 * u + e], o[2][2 * u + e], o[3][2 * u + e]);
-                    d[1] = make_float4(o[4][2 * u + e], o[5][2 * u + e], o[6][2 * u + e], o[7][2 * u + e]);
-                }
-            }
-            if (lane == 0) sm.piece[e2] = Piece{it, starts, ends};
+        if (lane == 0) {
+            if (whole) a.item[it] = make_int2(static_cast<int>(run), 1);
+            else sm.piece[e2] = Piece{it, starts, ends};
         }
         running = next_part(cur);
     }
@@ -518,8 +543,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             for (; e1 < 2 * WARPS && (sm.piece[e1].item == it || sm.piece[e1].item < 0); ++e1)
                 if (sm.piece[e1].item == it) tail = e1;
         if (it >= 0) {
-            const int h = static_cast<int>(it / a.tiles), row0 = static_cast<int>(it % a.tiles) * TILE;
-            const int live_rows = min(TILE, a.rows - row0);
+            const int h = static_cast<int>(it / a.tiles), row0 = static_cast<int>(it % a.tiles) * TR;
+            const int live_rows = min(TR, a.rows - row0);
             const long long run = it + blockIdx.x;
             const bool whole = sm.piece[e0].from_start && sm.piece[tail].to_end;
             for (int i = threadIdx.x; i < live_rows * (HD / 4); i += WARPS * 32) {
@@ -532,7 +557,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                     if (sm.piece[e].item != it) continue;
                     const float f = sm.m[e][r] == -INFINITY ? 0.f : ex2(sm.m[e][r] - M);
                     const float* src = (e & 1) ? reinterpret_cast<const float*>(&sm.ring[e >> 1][0][0][0])
-                                               : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + (e >> 1)) * TILE * HD;
+                                               : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + (e >> 1)) * TR * HD;
                     const float4 v = *reinterpret_cast<const float4*>(src + r * HD + 4 * q);
                     L = fmaf(sm.l[e][r], f, L);
                     s.x = fmaf(v.x, f, s.x);
@@ -540,7 +565,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                     s.z = fmaf(v.z, f, s.z);
                     s.w = fmaf(v.w, f, s.w);
                 }
-                if (q == 0) a.part_ml[run * TILE + r] = make_float2(M, L);
+                if (q == 0) a.part_ml[run * TR + r] = make_float2(M, L);
                 if (whole) {
                     const float inv = L == 0.f ? 0.f : 1.f / L;
                     const long long row = static_cast<long long>(h) * a.rows + row0 + r;
@@ -548,7 +573,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                         make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
                     if (q == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M - P_SHIFT + log2f(L)) * LN2;
                 } else {
-                    reinterpret_cast<float4*>(a.part_o + (run * TILE + r) * HD)[q] = s;
+                    reinterpret_cast<float4*>(a.part_o + (run * TR + r) * HD)[q] = s;
                 }
             }
         }
@@ -611,6 +636,7 @@ ZB_DEVINL void add_runs(const AttnArgs& a, int2 it, int r, int q, bool outputs, 
     }
 }
 
+template <int TR>
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     __shared__ float lse2[JOIN_ROWS];
     const zb_kv8& c = a.c;
@@ -631,10 +657,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     for (int r0 = 0; r0 < a.rows; r0 += 16) {
         const int row = r0 + r;
         if (row < a.rows) {
-            const int2 it = a.item[static_cast<long long>(h) * a.tiles + row / TILE];
+            const int2 it = a.item[static_cast<long long>(h) * a.tiles + row / TR];
             float M, L;
             float4 s;
-            add_runs<TILE>(a, it, row % TILE, q, part == 0, M, L, s);
+            add_runs<TR>(a, it, row % TR, q, part == 0, M, L, s);
             const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
             if (q == 0) lse2[row] = t;
             if (part == 0 && it.y > 1) {
@@ -716,7 +742,7 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
 
 // ------------------------------------------------------------------ host ----
 struct Plan {
-    long long rows, tiles, runs, groups;
+    long long rows, tile, tiles, runs, groups;
     size_t o, ml, item, gsum, lse2, total;
 };
 
@@ -727,11 +753,12 @@ constexpr int MAX_SMS = 256;
 Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
     Plan p{};
     p.rows = static_cast<long long>(heads_q / c.heads) * n_q;
-    p.tiles = (p.rows + TILE - 1) / TILE;
+    p.tile = p.rows <= 8 ? 8 : TILE;
+    p.tiles = (p.rows + p.tile - 1) / p.tile;
     p.runs = p.tiles * c.heads + MAX_SMS;           // an item and a CTA: their sum is its run
     p.groups = add_mass ? static_cast<long long>(c.slots) * (c.block > CHUNK ? c.block / CHUNK : 1) : 0;
-    p.o = up256(static_cast<size_t>(p.runs + MAX_SMS * WARPS) * TILE * HD * sizeof(float));
-    p.ml = up256(static_cast<size_t>(p.runs) * TILE * sizeof(float2));
+    p.o = up256(static_cast<size_t>(p.runs + MAX_SMS * WARPS) * p.tile * HD * sizeof(float));
+    p.ml = up256(static_cast<size_t>(p.runs) * p.tile * sizeof(float2));
     p.item = up256(static_cast<size_t>(p.tiles) * c.heads * sizeof(int2));
     p.gsum = up256(static_cast<size_t>(p.groups) * c.heads * p.rows * sizeof(float));
     p.lse2 = p.rows > JOIN_ROWS && add_mass ? up256(static_cast<size_t>(c.heads) * p.rows * sizeof(float)) : 0;
@@ -739,9 +766,9 @@ Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
     return p;
 }
 
-template <int FMT, bool ROWS8, int GK>
+template <int FMT, int NT, int GK>
 zb_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
-    auto* fn = attn_kernel<FMT, ROWS8, GK>;
+    auto* fn = attn_kernel<FMT, NT, GK>;
     static std::atomic<unsigned long long> done{0};  // devices that have the attribute set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ZB_ERR_CUDA;
@@ -753,17 +780,17 @@ zb_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
     fn<<<ctas, WARPS * 32, sizeof(AttnSmem), st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
 }
-template <int FMT, bool ROWS8>
+template <int FMT, int NT>
 zb_status launch_block(const AttnArgs& a, int ctas, cudaStream_t st) {
     switch (a.c.block) {
-        case 16: return launch_attn<FMT, ROWS8, 1>(a, ctas, st);
-        case 32: return launch_attn<FMT, ROWS8, 2>(a, ctas, st);
-        default: return launch_attn<FMT, ROWS8, 4>(a, ctas, st);
+        case 16: return launch_attn<FMT, NT, 1>(a, ctas, st);
+        case 32: return launch_attn<FMT, NT, 2>(a, ctas, st);
+        default: return launch_attn<FMT, NT, 4>(a, ctas, st);
     }
 }
 template <int FMT>
 zb_status launch_rows(const AttnArgs& a, int ctas, cudaStream_t st) {
-    return a.rows <= 8 ? launch_block<FMT, true>(a, ctas, st) : launch_block<FMT, false>(a, ctas, st);
+    return a.rows <= 8 ? launch_block<FMT, 1>(a, ctas, st) : launch_block<FMT, 2>(a, ctas, st);
 }
 
 }  // namespace kv8
@@ -833,6 +860,8 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         parts = (cache.slots + 255) / 256;
         if (parts > 64) parts = 64;
     }
-    kv8::join_kernel<<<dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)), 256, 0, st>>>(a);
+    const dim3 grid(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts));
+    if (p.tile == 8) kv8::join_kernel<8><<<grid, 256, 0, st>>>(a);
+    else kv8::join_kernel<kv8::TILE><<<grid, 256, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
 }
