@@ -14,8 +14,9 @@
 // each) across the heads it meets, and writes what lies wholly in its run at once:
 // the warps meet only at the end, where the CTA joins the parts of heads that
 // several of them hold.  (Joining at every head's end instead cost a batch with
-// some one-token sequences 3 us for each of them.)  What several CTAs hold goes to
-// the workspace, and the join kernel adds it up.
+// some one-token sequences 3 us for each of them.)  Starting on a head costs a warp
+// about as much as a chunk, so runs are equal in chunks and heads begun together.
+// What several CTAs hold goes to the workspace, and the join kernel adds it up.
 //
 // The codes go to the matrix instruction as fp16, which holds both formats
 // exactly; the scales stay in fp32 (s_k multiplies the logits, s_v the chunk's
@@ -83,17 +84,22 @@ struct __align__(128) AttnSmem {
 };
 
 // Where a warp stands in its run: the current item and the chunks of it that fall
-// into the run.
+// into the run.  Runs are measured in units: an item has one for its start and one
+// a chunk.
 struct Cursor {
     int h, tile;
     int c, c1;            // next chunk, end of the item's part
     int c0;               // first chunk of the item's part
     int nc;               // chunks of the item
     long long len;        // tokens of the head
-    long long left;       // chunks of the run after this part
+    long long left;       // units of the run after this part
 };
 
 ZB_DEVINL int chunks_of(long long len) { return static_cast<int>((len + CHUNK - 1) / CHUNK); }
+// Units of a head.
+ZB_DEVINL long long units_of(long long len, int tiles) {
+    return len > 0 ? static_cast<long long>(chunks_of(len) + 1) * tiles : 0;
+}
 
 // NT: groups of 8 query rows an item has.  GK: 16-key steps that share a value
 // scale (block / 16, at most 4).
@@ -110,11 +116,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     constexpr int PIECE_ROWS = CHUNK / PIECES;
     constexpr uint32_t PIECE_BYTES = PIECE_ROWS * HD;
 
-    // ---- this CTA's run: chunk counts of all heads, end to end -------------
+    // ---- this CTA's run: the units of all heads, end to end -----------------
     const int per = (c.heads + WARPS * 32 - 1) / (WARPS * 32);
     const int ha = min(static_cast<int>(threadIdx.x) * per, c.heads), hb = min(ha + per, c.heads);
     long long mine = 0;
-    for (int h = ha; h < hb; ++h) mine += static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+    for (int h = ha; h < hb; ++h) mine += units_of(head_len(a.lens, h, cap), a.tiles);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     if (before <= at && at < before + mine) {
         long long b = before;
         for (int h = ha; h < hb; ++h) {
-            const long long n = static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+            const long long n = units_of(head_len(a.lens, h, cap), a.tiles);
             if (at < b + n) {
                 sm.start_head = h;
                 sm.start_before = b;
@@ -150,25 +156,28 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     __syncthreads();
 
     auto open = [&](Cursor& k, int h, long long into, long long left) {
-        // position `into` of head h's chunks, `left` chunks to go in the run
+        // unit `into` of head h, `left` units to go in the run
         k.h = h;
         k.len = head_len(a.lens, h, cap);
         k.nc = chunks_of(k.len);
-        k.tile = static_cast<int>(into / k.nc);
-        k.c0 = static_cast<int>(into - static_cast<long long>(k.tile) * k.nc);
-        const long long here = min(left, static_cast<long long>(k.nc - k.c0));
-        k.c1 = k.c0 + static_cast<int>(here);
+        k.tile = static_cast<int>(into / (k.nc + 1));
+        const int u = static_cast<int>(into - static_cast<long long>(k.tile) * (k.nc + 1));
+        const int here = static_cast<int>(min(left, static_cast<long long>(k.nc + 1 - u)));
+        k.c0 = max(u - 1, 0);
+        k.c1 = u + here - 1;
         k.c = k.c0;
         k.left = left - here;
     };
-    auto next_part = [&](Cursor& k) -> bool {       // the run's next item
-        if (k.left == 0) return false;
-        int h = k.h, t = k.tile + 1;
-        if (t == a.tiles) {
-            t = 0;
-            do ++h; while (chunks_of(head_len(a.lens, h, cap)) == 0);
-        }
-        open(k, h, static_cast<long long>(t) * chunks_of(head_len(a.lens, h, cap)), k.left);
+    auto next_part = [&](Cursor& k) -> bool {       // the run's next item (a start without a chunk is none)
+        do {
+            if (k.left == 0) return false;
+            int h = k.h, t = k.tile + 1;
+            if (t == a.tiles) {
+                t = 0;
+                do ++h; while (head_len(a.lens, h, cap) == 0);
+            }
+            open(k, h, static_cast<long long>(t) * (chunks_of(head_len(a.lens, h, cap)) + 1), k.left);
+        } while (k.c0 >= k.c1);
         return true;
     };
     // this warp's run within the CTA's, and the head it starts in
@@ -180,16 +189,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         int h = sm.start_head;
         long long b = sm.start_before;
         for (;; ++h) {
-            const long long n = static_cast<long long>(chunks_of(head_len(a.lens, h, cap))) * a.tiles;
+            const long long n = units_of(head_len(a.lens, h, cap), a.tiles);
             if (wa < b + n) break;
             b += n;
         }
         open(cur, h, wa - b, wb - wa);
+        if (cur.c0 >= cur.c1) running = next_part(cur);
         iss = cur;
     }
     bool more = running;                             // the issue cursor stands on a chunk
     auto settle = [&]() {
-        if (iss.c >= iss.c1) more = next_part(iss);
+        if (iss.c < iss.c1) return;
+        more = next_part(iss);
+        // the next item's queries, ahead of their use
+        const int r = iss.tile * TR + lane;
+        if (more && lane < TR && r < a.rows)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(a.Q + (static_cast<long long>(iss.h) * a.rows + r) * HD));
     };
 
     const WaitCtx wc{a.status, &sm.abort_flag, a.timeout_ns};
@@ -584,7 +599,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         const Piece p = sm.piece[2 * warp + lane];
         // a part that begins an item is the warp's last, and ends where its run ends
         const long long len = head_len(a.lens, static_cast<int>(p.item / a.tiles), cap);
-        const long long final = wb - (cur.c1 - cur.c0) + chunks_of(len) - 1;
+        const long long final = wb - (cur.c1 - cur.c0) + chunks_of(len) - 1;   // the last chunk's unit
         const long long to = ((final + 1) * ctas - 1) / total;
         a.item[p.item] = make_int2(static_cast<int>(p.item + blockIdx.x), static_cast<int>(to - blockIdx.x + 1));
     }
