@@ -106,6 +106,7 @@ ZB_DEVINL long long units_of(long long len, int tiles) {
 template <int FMT, int NT, int GK>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     constexpr int TR = 8 * NT;
+    let_next_start();
     extern __shared__ uint8_t smem_raw[];
     AttnSmem& sm = *reinterpret_cast<AttnSmem*>(smem_raw);
     const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c4 = lane & 3;
@@ -658,6 +659,28 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     const int h = blockIdx.x, part = blockIdx.y;
     const long long cap = static_cast<long long>(c.slots) * c.block;
     const long long len = head_len(a.lens, h, cap);
+    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
+    const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
+    const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
+    const int first = part * 256 + threadIdx.x;      // this thread's first block
+    // what the attention kernel does not write is read while it still runs
+    float* mass = nullptr;
+    float old = 0.f;
+    if (a.groups && first < blocks) {
+        mass = c.mass + static_cast<long long>(h) * c.slots + slot_of(c, h, first, a.status);
+        old = *mass;
+    }
+    wait_for_previous();
+    // and the block's group sums while the rows' sums are added up
+    constexpr int AHEAD = 16;
+    const bool few = per_block * a.rows <= AHEAD;
+    float gs[AHEAD];
+    const int sums = a.groups && first < blocks ? (min((first + 1) * per_block, live) - first * per_block) * a.rows : 0;
+    const float* gsum = a.gsum + (static_cast<long long>(h) * a.groups + static_cast<long long>(first) * per_block) * a.rows;
+    if (few) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) gs[i] = i < sums ? gsum[i] : -INFINITY;
+    }
     if (len == 0) {
         if (part) return;
         for (int i = threadIdx.x; i < a.rows * (HD / 8); i += 256) {
@@ -689,18 +712,27 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     }
     if (!a.groups) return;
     __syncthreads();
-    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
-    const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
-    const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
-    for (int b = part * 256 + threadIdx.x; b < blocks; b += gridDim.y * 256) {
+    for (int b = first; b < blocks; b += gridDim.y * 256) {
         float s = 0.f;
-        for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
-            const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
-            for (int i = 0; i < a.rows; ++i)
-                if (lse2[i] != -INFINITY) s += ex2(gs[i] - lse2[i]);
+        if (few && b == first) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (i >= sums) break;
+                const float t = lse2[i % a.rows];
+                if (t != -INFINITY) s += ex2(gs[i] - t);
+            }
+        } else {
+            for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
+                const float* gk = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
+                for (int i = 0; i < a.rows; ++i)
+                    if (lse2[i] != -INFINITY) s += ex2(gk[i] - lse2[i]);
+            }
         }
-        const int slot = slot_of(c, h, b, a.status);
-        c.mass[static_cast<long long>(h) * c.slots + slot] += s;
+        if (b != first) {
+            mass = c.mass + static_cast<long long>(h) * c.slots + slot_of(c, h, b, a.status);
+            old = *mass;
+        }
+        *mass = old + s;
     }
 }
 
@@ -708,6 +740,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
 // a block for the weights (a head's rows are contiguous in its group sums).
 template <int TR>
 __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
+    wait_for_previous();
+    let_next_start();
     const zb_kv8& c = a.c;
     const int h = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
     const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
@@ -730,6 +764,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
 }
 
 __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
+    wait_for_previous();
     const zb_kv8& c = a.c;
     const int h = blockIdx.x;
     const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
@@ -862,13 +897,12 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
     if (e != ZB_OK) return e;
     if (p.rows > kv8::JOIN_ROWS) {
         if (add_mass) a.lse2 = reinterpret_cast<float*>(w + p.o + p.ml + p.item + p.gsum);
-        kv8::join_rows_kernel<kv8::TILE><<<static_cast<unsigned>(cache.heads * p.tiles), 256, 0, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
-        if (add_mass) {
-            const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
-            kv8::mass_kernel<<<dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)), 256, 0, st>>>(a);
-        }
-        return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+        e = kv8::launch_behind(kv8::join_rows_kernel<kv8::TILE>, dim3(static_cast<unsigned>(cache.heads * p.tiles)), 256,
+                               st, a);
+        if (e != ZB_OK || !add_mass) return e;
+        const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
+        return kv8::launch_behind(kv8::mass_kernel, dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)),
+                                  256, st, a);
     }
     int parts = 1;
     if (a.groups) {
@@ -876,7 +910,5 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         if (parts > 64) parts = 64;
     }
     const dim3 grid(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts));
-    if (p.tile == 8) kv8::join_kernel<8><<<grid, 256, 0, st>>>(a);
-    else kv8::join_kernel<kv8::TILE><<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+    return kv8::launch_behind(p.tile == 8 ? kv8::join_kernel<8> : kv8::join_kernel<kv8::TILE>, grid, 256, st, a);
 }
