@@ -300,9 +300,9 @@ __global__ void __launch_bounds__(256) read_kernel(const zb_kv8 c, const int32_t
 }
 
 // ----------------------------------------------------------------- evict ----
-constexpr int E_THREADS = 1024;
 constexpr int E_BINS = 2048;
-constexpr int E_KEYS = 40960;    // keys kept in shared memory; longer lists gather them again
+constexpr int E_ITEMS = 24576;   // blocks whose keys and slots fit shared memory; longer lists gather them again
+constexpr int E_AHEAD = 12;      // gathers a thread has in flight
 
 // Order-preserving key of a weight (NaN with a clear sign above +inf; -0 as +0).
 ZB_DEVINL uint32_t mass_key(float m) {
@@ -316,7 +316,7 @@ struct EvictArgs {
     const int32_t* lens;
     int slots, block, budget, sinks, recent;
     int32_t *table_out, *lens_out, *kept;
-    int keys_in_smem;
+    int in_smem;
     int* status;
 };
 
@@ -325,12 +325,18 @@ struct EvictArgs {
 // to the bin that holds the last kept one until it is a single value (at most
 // three rounds), then one pass that keeps everything above it and the lowest
 // indices among equals, each warp writing its own contiguous part in order.
-// Bound by latency: a few dependent rounds over a list of some thousand words.
-__global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t keys[];
+// Bound by latency: two dependent gathers (slot, weight), then rounds over a list
+// of some thousand words in shared memory.  256 threads serve lists of up to 2,048
+// blocks, so that several heads share an SM (384 heads of 344 blocks: 13 -> %s us);
+// 1,024 the longer ones (16 heads of 10,992: 16 -> %s us, with E_AHEAD gathers of a
+// thread in flight and the slots kept).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t items[];              // keys, then slots
+    constexpr int W = THREADS / 32, PER = E_BINS / THREADS;
     __shared__ uint32_t hist[E_BINS];
     __shared__ uint32_t red[32], red2[32];
-    __shared__ uint32_t s_lo, s_bin, s_above;
+    __shared__ uint32_t s_bin, s_above;
     const int h = blockIdx.x, tid = threadIdx.x, lane = lane_id(), warp = warp_id();
     const long long row = static_cast<long long>(h) * a.slots;
     const int32_t* table = a.table + row;
@@ -339,28 +345,48 @@ __global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
     const long long len = head_len(a.lens, h, static_cast<long long>(a.slots) * a.block);
     const int nb = static_cast<int>((len + a.block - 1) / a.block);
     if (nb <= a.budget) {
-        for (int b = tid; b < a.slots; b += E_THREADS) out[b] = table[b];
+        for (int b = tid; b < a.slots; b += THREADS) out[b] = table[b];
         if (kept)
-            for (int b = tid; b < a.budget; b += E_THREADS) kept[b] = b < nb ? b : -1;
+            for (int b = tid; b < a.budget; b += THREADS) kept[b] = b < nb ? b : -1;
         if (tid == 0) a.lens_out[h] = static_cast<int32_t>(len);
         return;
     }
     const int b0 = a.sinks, b1 = nb - a.recent;
     const int need = a.budget - a.sinks - a.recent;   // < b1 - b0
-    auto gather = [&](int b) -> uint32_t {
-        const int s = table[b];
+    uint32_t* keys = items;
+    uint32_t* slots = items + a.slots;
+    auto key_of = [&](int s) -> uint32_t {
         if (s < 0 || s >= a.slots) {
             flag_status(a.status, ZB_ERR_INDEX);
             return 0u;
         }
-        return mass_key(a.mass[row + s]);
+        return mass_key(__ldg(a.mass + row + s));
     };
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int b = b0 + tid; b < b1; b += E_THREADS) {
-        const uint32_t k = gather(b);
-        if (a.keys_in_smem) keys[b] = k;
-        lo = min(lo, k);
-        hi = max(hi, k);
+    for (int base = tid; base < a.slots; base += THREADS * E_AHEAD) {
+        int s[E_AHEAD];
+        uint32_t k[E_AHEAD];
+#pragma unroll
+        for (int i = 0; i < E_AHEAD; ++i) s[i] = base + i * THREADS < a.slots ? __ldg(table + base + i * THREADS) : 0;
+#pragma unroll
+        for (int i = 0; i < E_AHEAD; ++i) {
+            const int b = base + i * THREADS;
+            k[i] = b >= b0 && b < b1 ? key_of(s[i]) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < E_AHEAD; ++i) {
+            const int b = base + i * THREADS;
+            if (b >= a.slots) continue;
+            if (b >= b0 && b < b1) {
+                lo = min(lo, k[i]);
+                hi = max(hi, k[i]);
+            }
+            if (a.in_smem) {
+                keys[b] = k[i];
+                slots[b] = s[i];
+            }
+            if (b >= nb) out[b] = s[i];              // unused slots stay
+        }
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
@@ -368,30 +394,35 @@ __global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
         red[warp] = lo;
         red2[warp] = hi;
     }
+    for (int i = tid; i < E_BINS; i += THREADS) hist[i] = 0;
     __syncthreads();
-    lo = __reduce_min_sync(0xffffffffu, red[lane]);
-    hi = __reduce_max_sync(0xffffffffu, red2[lane]);
+    lo = __reduce_min_sync(0xffffffffu, lane < W ? red[lane] : 0xFFFFFFFFu);
+    hi = __reduce_max_sync(0xffffffffu, lane < W ? red2[lane] : 0u);
     __syncthreads();
-    auto key = [&](int b) -> uint32_t { return a.keys_in_smem ? keys[b] : gather(b); };
+    auto slot = [&](int b) -> int { return a.in_smem ? static_cast<int>(slots[b]) : table[b]; };
+    auto key = [&](int b) -> uint32_t { return a.in_smem ? keys[b] : key_of(table[b]); };
 
     // invariant: `want` keys are to be kept of those in [lo, hi] (the larger ones,
-    // above hi, are all kept already), 0 <= want <= their number
+    // above hi, are all kept already), 0 <= want <= their number; hist is zero
     uint32_t want = need;
     while (need > 0 && lo < hi) {
         const uint32_t span = hi - lo;
         const int bits = 32 - __clz(span);
         const int sh = bits > 11 ? bits - 11 : 0;
-        for (int i = tid; i < E_BINS; i += E_THREADS) hist[i] = 0;
-        __syncthreads();
-        for (int b = b0 + tid; b < b1; b += E_THREADS) {
+        for (int b = b0 + tid; b < b1; b += THREADS) {
             const uint32_t k = key(b);
             if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> sh], 1u);
         }
         __syncthreads();
-        // two bins a thread, from the top: the bin where the count reaches `want`
-        const int bin = E_BINS - 2 - 2 * tid;
-        const uint32_t c1 = hist[bin + 1], c0 = hist[bin];
-        uint32_t incl = c0 + c1;
+        // PER bins a thread, from the top: the bin where the count reaches `want`
+        const int top = E_BINS - 1 - PER * tid;
+        uint32_t c[PER], own = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            c[i] = hist[top - i];
+            own += c[i];
+        }
+        uint32_t incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -399,29 +430,31 @@ __global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
         }
         if (lane == 31) red[warp] = incl;
         __syncthreads();
-        uint32_t before = lane < warp ? red[lane] : 0;
-        before = __reduce_add_sync(0xffffffffu, before) + incl - c0 - c1;   // kept above this thread's bins
-        if (before < want && want <= before + c1) {
-            s_bin = bin + 1;
-            s_above = before;
-        } else if (before + c1 < want && want <= before + c1 + c0) {
-            s_bin = bin;
-            s_above = before + c1;
+        uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0) + incl - own;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (before < want && want <= before + c[i]) {
+                s_bin = top - i;
+                s_above = before;
+            }
+            before += c[i];
+            hist[top - i] = 0;
         }
         __syncthreads();
         want -= s_above;
         lo += s_bin << sh;
         const uint32_t width = (1u << sh) - 1u;
         if (hi - lo > width) hi = lo + width;
-        __syncthreads();
     }
+    __syncthreads();
     // keep: keys above `hi` (== lo) and the first `want` equal to it
     const uint32_t edge = need > 0 ? lo : 0xFFFFFFFFu;
     if (need == 0) want = 0;
-    const int per = ((nb + 1023) / 1024) * 32;            // blocks a warp takes
+    const int per = ((nb + THREADS - 1) / THREADS) * 32;  // blocks a warp takes
     const int w0 = min(warp * per, nb), w1 = min(w0 + per, nb);
+    const int w2 = w0 + (w1 - w0 + 31) / 32 * 32;         // all lanes run the same rounds
     uint32_t over = 0, ties = 0;
-    for (int b = w0 + lane; b < w1 + ((32 - (w1 - w0) % 32) & 31); b += 32) {
+    for (int b = w0 + lane; b < w2; b += 32) {
         const bool in = b < w1, mid = in && b >= b0 && b < b1;
         const uint32_t k = mid ? key(b) : 0u;
         over += __popc(__ballot_sync(0xffffffffu, in && (!mid || k > edge)));
@@ -435,7 +468,7 @@ __global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
     const uint32_t over0 = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane] : 0);
     uint32_t ties0 = __reduce_add_sync(0xffffffffu, lane < warp ? red2[lane] : 0);
     uint32_t pos = over0 + min(ties0, want);              // kept before this warp's part
-    for (int b = w0 + lane; b < w1 + ((32 - (w1 - w0) % 32) & 31); b += 32) {
+    for (int b = w0 + lane; b < w2; b += 32) {
         const bool in = b < w1, mid = in && b >= b0 && b < b1;
         const uint32_t k = mid ? key(b) : 0u;
         const uint32_t below = (1u << lane) - 1u;
@@ -445,16 +478,15 @@ __global__ void __launch_bounds__(E_THREADS) evict_kernel(const EvictArgs a) {
         if (in) {
             const uint32_t r = pos + __popc(mask & below);   // kept blocks before b
             if (keep) {
-                out[r] = table[b];
+                out[r] = slot(b);
                 if (kept) kept[r] = b;
             } else {
-                out[a.budget + (b - r)] = table[b];
+                out[a.budget + (b - r)] = slot(b);
             }
         }
         pos += __popc(mask);
         ties0 += __popc(tie);
     }
-    for (int b = nb + tid; b < a.slots; b += E_THREADS) out[b] = table[b];
     if (tid == 0) a.lens_out[h] = static_cast<int32_t>(len - static_cast<long long>(nb - a.budget) * a.block);
 }
 
@@ -530,12 +562,16 @@ extern "C" zb_status zb_kv8_evict(const int32_t* table, const float* mass, const
     zb_status e = current_device(&dev);
     if (e != ZB_OK) return e;
     kv8::EvictArgs a{table, mass, lens, slots, block, budget, sinks, recent, table_out, lens_out, kept,
-                     slots <= kv8::E_KEYS, dev.status};
-    const int smem = a.keys_in_smem ? slots * 4 : 0;
-    if (smem > 32 * 1024 &&
-        cudaFuncSetAttribute(kv8::evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kv8::E_KEYS * 4) !=
-        cudaSuccess)
-        return ZB_ERR_CUDA;
-    kv8::evict_kernel<<<heads, kv8::E_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(a);
+                     slots <= kv8::E_ITEMS, dev.status};
+    const int smem = a.in_smem ? slots * 8 : 0;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (slots <= 2048) {
+        kv8::evict_kernel<256><<<heads, 256, smem, st>>>(a);
+    } else {
+        if (smem > 32 * 1024 && cudaFuncSetAttribute(kv8::evict_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kv8::E_ITEMS * 8) != cudaSuccess)
+            return ZB_ERR_CUDA;
+        kv8::evict_kernel<1024><<<heads, 1024, smem, st>>>(a);
+    }
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
 }
