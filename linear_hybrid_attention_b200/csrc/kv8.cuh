@@ -19,6 +19,29 @@ constexpr float LN2 = 0.6931471805599453f;
 // keys of negligible weight each add up to what they should.
 constexpr float P_SHIFT = 14.f;
 
+// What the attention kernels (kv8_attn.cu for few query rows a head, kv8_tile.cu for
+// many) and those that join their partial results are given.
+struct AttnArgs {
+    zb_kv8 c;
+    const uint16_t* Q;
+    uint16_t* O;
+    float* lse;
+    const int32_t* lens;
+    int rows, n_q, tiles;        // query rows a head (its group's heads x n_q), items a head
+    int causal;
+    float scale_log2;
+    long long runs;              // partial results of CTAs; those of single warps follow
+    int groups;                  // weight sums a head: runs of min(block, 64) keys, or 0
+    // workspace
+    float* part_o;               // [runs, then one a warp][tile][64]
+    float2* part_ml;             // [...][tile]: running maximum (log2 units) and sum
+    int2* item;                  // [heads * tiles]: first partial run, number of runs
+    float* gsum;                 // [heads][groups][rows]: log2 of a row's sum over a group
+    float* lse2;                 // [heads][rows]: log2 of a row's whole sum (many rows)
+    int* status;
+    unsigned long long timeout_ns;
+};
+
 // Tokens of head h, cut to what the cache can hold.
 ZB_DEVINL long long head_len(const int32_t* lens, int h, long long cap) {
     const long long n = __ldg(lens + h);
@@ -104,6 +127,9 @@ ZB_DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "me
 ZB_DEVINL void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------ host side ----
+// kv8_tile.cu: attention of many rows and the join of its parts (pair: items of 256 rows, else 128).
+zb_status launch_tiles(const AttnArgs& a, bool pair, int ctas, cudaStream_t st);
+
 template <class... P, class... A>
 inline zb_status launch_behind(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};

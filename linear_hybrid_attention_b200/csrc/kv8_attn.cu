@@ -43,27 +43,6 @@ constexpr int STAGES = 2;
 constexpr int TILE = 16;                         // most query rows of an item (8 if there are no more)
 constexpr uint32_t HALF_STAGE = CHUNK * HD;      // 4 KB of codes
 
-struct AttnArgs {
-    zb_kv8 c;
-    const uint16_t* Q;
-    uint16_t* O;
-    float* lse;
-    const int32_t* lens;
-    int rows, n_q, tiles;        // query rows a head (its group's heads x n_q), items a head
-    int causal;
-    float scale_log2;
-    long long runs;              // partial results of CTAs; those of single warps follow
-    int groups;                  // weight sums a head: runs of min(block, 64) keys, or 0
-    // workspace
-    float* part_o;               // [runs, then one a warp][tile][64]
-    float2* part_ml;             // [...][tile]: running maximum (log2 units) and sum
-    int2* item;                  // [heads * tiles]: first partial run, number of runs
-    float* gsum;                 // [heads][groups][rows]: log2 of a row's sum over a group
-    float* lse2;                 // [heads][rows]: log2 of a row's whole sum (more than JOIN_ROWS rows)
-    int* status;
-    unsigned long long timeout_ns;
-};
-
 // A warp's part of an item that others hold parts of too (item -1: none).  Entry 2 w
 // is the part that warp w's run starts with, in its row of part_o; entry 2 w + 1 the
 // part it ends with, in its ring.
@@ -611,7 +590,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
 // with a.groups, turns the rows' group sums into the blocks' weight.  Grid: (heads,
 // parts): every part works out the rows' log-sum-exp again, part 0 writes the
 // outputs, and the blocks are shared out over the parts.
-constexpr int JOIN_ROWS = 32;
+constexpr int FEW_ROWS = 32;                     // most rows a head that this kernel takes; kv8_tile.cu takes more
+constexpr int JOIN_ROWS = FEW_ROWS;
 
 // One row's runs added up, by the 16 threads (one half warp) that hold 4 of its
 // features each: each thread reads the maximum and sum of one run in sixteen, so a
@@ -736,33 +716,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     }
 }
 
-// The same for more rows, in two launches: the rows of one item a CTA, then a warp
-// a block for the weights (a head's rows are contiguous in its group sums).
-template <int TR>
-__global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
-    wait_for_previous();
-    let_next_start();
-    const zb_kv8& c = a.c;
-    const int h = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-    const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
-    const int2 it = len ? a.item[blockIdx.x] : make_int2(0, 0);
-    const int q = threadIdx.x & 15;
-    for (int r = threadIdx.x >> 4; r < TR && tile * TR + r < a.rows; r += 16) {
-        float M, L;
-        float4 s;
-        add_runs<TR>(a, it, r, q, true, M, L, s);
-        const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
-        const long long row = static_cast<long long>(h) * a.rows + tile * TR + r;
-        if (q == 0 && a.lse2) a.lse2[row] = t;
-        if (it.y != 1) {                             // an item of one run has been written already
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            reinterpret_cast<uint2*>(a.O + row * HD)[q] =
-                make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
-            if (q == 0 && a.lse) a.lse[row] = t * LN2;
-        }
-    }
-}
-
+// The weights for more rows (kv8_tile.cu): a warp a block, whose rows' sums are
+// contiguous.  A causal row's sums end where its keys do.
 __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     wait_for_previous();
     const zb_kv8& c = a.c;
@@ -771,14 +726,16 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     const int blocks = static_cast<int>((len + c.block - 1) / c.block);
     const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
     const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
+    const int size = min(c.block, CHUNK);
     const float* lse2 = a.lse2 + static_cast<long long>(h) * a.rows;
     for (int b = blockIdx.y * 8 + warp_id(); b < blocks; b += gridDim.y * 8) {
         float s = 0.f;
         for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
             const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
             for (int i = lane_id(); i < a.rows; i += 32) {
-                const float t = __ldg(lse2 + i);
-                if (t != -INFINITY) s += ex2(gs[i] - t);
+                const float t = lse2[i];
+                const bool sees = !a.causal || static_cast<long long>(k) * size < len - a.n_q + 1 + i % a.n_q;
+                if (sees && t != -INFINITY) s += ex2(gs[i] - t);
             }
         }
 #pragma unroll
@@ -792,26 +749,30 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
 
 // ------------------------------------------------------------------ host ----
 struct Plan {
+    bool few, pair;       // the streaming kernel; else 256 rows an item, or 128
     long long rows, tile, tiles, runs, groups;
     size_t o, ml, item, gsum, lse2, total;
 };
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-constexpr int MAX_SMS = 256;
+constexpr int MAX_SMS = 160;
 
 Plan plan(const zb_kv8& c, int heads_q, long long n_q, int add_mass) {
     Plan p{};
     p.rows = static_cast<long long>(heads_q / c.heads) * n_q;
-    p.tile = p.rows <= 8 ? 8 : TILE;
+    p.few = p.rows <= FEW_ROWS;
+    p.pair = p.rows > 128;
+    p.tile = p.few ? (p.rows <= 8 ? 8 : TILE) : p.pair ? 256 : 128;
     p.tiles = (p.rows + p.tile - 1) / p.tile;
-    p.runs = p.tiles * c.heads + MAX_SMS;           // an item and a CTA: their sum is its run
+    // few rows: an item and a CTA, their sum is its run, and a row a warp; many: two places a CTA
+    p.runs = p.few ? p.tiles * c.heads + MAX_SMS : 2 * MAX_SMS;
     p.groups = add_mass ? static_cast<long long>(c.slots) * (c.block > CHUNK ? c.block / CHUNK : 1) : 0;
-    p.o = up256(static_cast<size_t>(p.runs + MAX_SMS * WARPS) * p.tile * HD * sizeof(float));
+    p.o = up256(static_cast<size_t>(p.runs + (p.few ? MAX_SMS * WARPS : 0)) * p.tile * HD * sizeof(float));
     p.ml = up256(static_cast<size_t>(p.runs) * p.tile * sizeof(float2));
     p.item = up256(static_cast<size_t>(p.tiles) * c.heads * sizeof(int2));
     p.gsum = up256(static_cast<size_t>(p.groups) * c.heads * p.rows * sizeof(float));
-    p.lse2 = p.rows > JOIN_ROWS && add_mass ? up256(static_cast<size_t>(c.heads) * p.rows * sizeof(float)) : 0;
+    p.lse2 = !p.few && add_mass ? up256(static_cast<size_t>(c.heads) * p.rows * sizeof(float)) : 0;
     p.total = p.o + p.ml + p.item + p.gsum + p.lse2;
     return p;
 }
@@ -892,18 +853,17 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
     a.status = dev.status;
     a.timeout_ns = wait_timeout_ns();
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = cache.format == ZB_KV8_INT8 ? kv8::launch_rows<ZB_KV8_INT8>(a, dev.sm_count, st)
-                                    : kv8::launch_rows<ZB_KV8_E4M3>(a, dev.sm_count, st);
-    if (e != ZB_OK) return e;
-    if (p.rows > kv8::JOIN_ROWS) {
+    if (!p.few) {
         if (add_mass) a.lse2 = reinterpret_cast<float*>(w + p.o + p.ml + p.item + p.gsum);
-        e = kv8::launch_behind(kv8::join_rows_kernel<kv8::TILE>, dim3(static_cast<unsigned>(cache.heads * p.tiles)), 256,
-                               st, a);
+        e = kv8::launch_tiles(a, p.pair, dev.sm_count, st);
         if (e != ZB_OK || !add_mass) return e;
         const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
         return kv8::launch_behind(kv8::mass_kernel, dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)),
                                   256, st, a);
     }
+    e = cache.format == ZB_KV8_INT8 ? kv8::launch_rows<ZB_KV8_INT8>(a, dev.sm_count, st)
+                                    : kv8::launch_rows<ZB_KV8_E4M3>(a, dev.sm_count, st);
+    if (e != ZB_OK) return e;
     int parts = 1;
     if (a.groups) {
         parts = (cache.slots + 255) / 256;

@@ -1,0 +1,728 @@
+// Softmax attention over the 8-bit key/value cache for many query rows a head (a
+// view's or a prompt's tokens at once), on the tcgen05 tensor cores.
+//
+// The same mathematics as kv8_attn.cu, bound by the exponentials and the
+// instructions around them rather than by the cache's bytes.  One persistent CTA
+// per SM, 512 threads:
+//   warp 0        loader: bulk copies of a 128-key tile's codes into a ring, and
+//                 the tile's scales, 16 keys to an entry
+//   warps 1, 2    MMA issuers of row tiles ("slots") 0 and 1: S = Q K^T, O += P V
+//   warps 4..7    converters (two for K, two for V): codes to fp16, exactly, in the
+//                 128-byte-swizzle layout the MMAs read
+//   warps 8..11, 12..15  softmax of slots 0 and 1, one thread a row
+// Work items are 256 query rows of a head, 128 in each slot, both slots reading
+// every converted tile (half the conversions a row); or 128 rows, where a head has
+// no more, with the tiles dealt to the slots in turn.  Items are laid end to end in
+// tiles, and each CTA takes an equal run, as in kv8_attn.cu; a causal item ends
+// with its last row's last key.  Only the first and the last part of a run can be
+// less than an item: those go to the workspace, to the CTA's two places there, and a
+// second kernel adds them up.
+//
+// Scales.  s_k multiplies the logits, per 16 columns.  s_v rides in the exponent:
+// P = 2^(x + log2 s_v - m), so that O += P code needs no further product, and the
+// softmax sum takes each 16 columns' sum of P times 1 / s_v.  The running reference
+// m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "kv8.cuh"
+
+namespace zb {
+namespace kv8 {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int THREADS = 512;
+constexpr int RAW = 3, K16 = 3, V16 = 3, SC = 4;   // ring stages
+constexpr uint32_t RAW_BYTES = BN * HD;            // 8 KB of codes
+constexpr uint32_t TILE_BYTES = BN * HD * 2;       // 16 KB of fp16
+constexpr uint32_t TMEM_COLS = 512, SLOT_COLS = 256, TM_S = 0, TM_P = 128, TM_O = 192;
+constexpr uint32_t SLEEP_NS = 20000;
+// 128 threads each of roles and converters, 256 of softmax; adds up to the launch's 512 x 128
+constexpr int LAUNCH_REGS = 128, ROLE_REGS = 40, CONVERT_REGS = 72, SOFTMAX_REGS = 200;
+static_assert(128 * (ROLE_REGS + CONVERT_REGS) + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
+// P is at most 2^(SHIFT + RAISE) in fp16 and rounded to 2^-11 of its value down to
+// 2^-(SHIFT + 14) of the reference, to 2^-(SHIFT + 25) of it below.
+constexpr float SHIFT = 11.f, RAISE = 4.f;
+
+struct __align__(1024) TileSmem {
+    uint8_t q[2][TILE_BYTES];
+    uint8_t k16[K16][TILE_BYTES];
+    uint8_t v16[V16][TILE_BYTES];
+    uint8_t raw[RAW][2][RAW_BYTES];
+    float4 other[HD / 4][BM];         // slot 1's sums where it shares slot 0's rows
+    float2 other_ml[BM];
+    float4 sc[SC][8];                 // s_k, log2 s_v, 1 / s_v of 16 keys
+    uint32_t sc_nan[SC];              // bit g: s_v of group g is not finite
+    uint64_t raw_full[RAW], raw_empty[RAW];
+    uint64_t k_full[K16], k_empty[K16], v_full[V16], v_empty[V16];
+    uint64_t sc_full[SC], sc_empty[SC];
+    uint64_t other_full, other_empty;
+    uint64_t q_full[2], s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
+    unsigned long long wsum[THREADS / 32];
+    long long start_before;
+    long long start_item;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int N>
+ZB_DEVINL void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+ZB_DEVINL void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+ZB_DEVINL void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Instruction descriptor: fp16 A and B, fp32 accumulator (b_mn: B stored along N).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Tiles of an item: those its last-reaching row sees.
+ZB_DEVINL int item_tiles(const AttnArgs& a, long long len, int tile, int item_rows) {
+    if (a.causal) {
+        const long long r0 = static_cast<long long>(tile) * item_rows;
+        const long long r1 = min(r0 + item_rows, static_cast<long long>(a.rows)) - 1;
+        const long long reach = r0 / a.n_q == r1 / a.n_q ? r1 % a.n_q : a.n_q - 1;
+        len = min(len, max(len - a.n_q + 1 + reach, 0ll));
+    }
+    return static_cast<int>((len + BN - 1) / BN);
+}
+
+// Units of an item in the runs: two for its start (Q, and a pipeline that runs
+// empty) and one a tile.
+constexpr int START = 2;
+ZB_DEVINL long long item_units(int tiles) { return tiles ? tiles + START : 0; }
+
+// The parts of items that make up a CTA's run, in order; every role walks them.
+struct Walk {
+    long long item, left;     // units of the run after this part
+    int h, tile, c0, c1, nc;
+    long long len;
+};
+
+template <bool PAIR>
+struct Items {
+    static constexpr int ROWS = PAIR ? 256 : 128;
+    const AttnArgs& a;
+    long long cap;
+    ZB_DEVINL void load(Walk& w, long long item, long long into, long long left) const {
+        w.item = item;
+        w.h = static_cast<int>(item / a.tiles);
+        w.tile = static_cast<int>(item - static_cast<long long>(w.h) * a.tiles);
+        w.len = head_len(a.lens, w.h, cap);
+        w.nc = item_tiles(a, w.len, w.tile, ROWS);
+        const long long here = min(left, item_units(w.nc) - into);
+        w.c0 = max(static_cast<int>(into) - START, 0);
+        w.c1 = max(static_cast<int>(into + here) - START, 0);
+        w.left = left - here;
+    }
+    // To the next part with a tile in it; false at the run's end.
+    ZB_DEVINL bool next(Walk& w) const {
+        do {
+            if (w.left == 0) return false;
+            long long item = w.item + 1;
+            while (item_tiles(a, head_len(a.lens, static_cast<int>(item / a.tiles), cap),
+                              static_cast<int>(item % a.tiles), ROWS) == 0)
+                ++item;
+            load(w, item, 0, w.left);
+        } while (w.c0 >= w.c1);
+        return true;
+    }
+};
+
+template <int FMT, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
+    let_next_start();
+    extern __shared__ uint8_t smem_raw[];
+    TileSmem& sm = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = warp_id(), lane = lane_id();
+    const zb_kv8& c = a.c;
+    const int B = c.block, shift = 31 - __clz(B);
+    const long long cap = static_cast<long long>(c.slots) * B;
+    const Items<PAIR> items{a, cap};
+    const WaitCtx wc{a.status, &sm.abort_flag, a.timeout_ns};
+
+    // ---- this CTA's run ------------------------------------------------------
+    const long long n_items = static_cast<long long>(c.heads) * a.tiles;
+    const long long per = (n_items + THREADS - 1) / THREADS;
+    const long long ia = min(threadIdx.x * per, n_items), ib = min(ia + per, n_items);
+    auto units = [&](long long i) {
+        return item_units(item_tiles(a, head_len(a.lens, static_cast<int>(i / a.tiles), cap),
+                                     static_cast<int>(i % a.tiles), Items<PAIR>::ROWS));
+    };
+    long long mine = 0;
+    for (long long i = ia; i < ib; ++i) mine += units(i);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    if (threadIdx.x == 0) {
+        sm.abort_flag = 0;
+        for (int i = 0; i < RAW; ++i) {
+            mbar_init(smem_addr(&sm.raw_full[i]), 1);
+            mbar_init(smem_addr(&sm.raw_empty[i]), 4);
+        }
+        for (int i = 0; i < K16; ++i) {
+            mbar_init(smem_addr(&sm.k_full[i]), 2);
+            mbar_init(smem_addr(&sm.k_empty[i]), PAIR ? 2 : 1);
+        }
+        for (int i = 0; i < V16; ++i) {
+            mbar_init(smem_addr(&sm.v_full[i]), 2);
+            mbar_init(smem_addr(&sm.v_empty[i]), PAIR ? 2 : 1);
+        }
+        for (int i = 0; i < SC; ++i) {
+            mbar_init(smem_addr(&sm.sc_full[i]), 1);
+            mbar_init(smem_addr(&sm.sc_empty[i]), PAIR ? 8 : 4);
+        }
+        mbar_init(smem_addr(&sm.other_full), 128);
+        mbar_init(smem_addr(&sm.other_empty), 128);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&sm.q_full[s]), 128);
+            mbar_init(smem_addr(&sm.s_full[s]), 1);
+            mbar_init(smem_addr(&sm.s_free[s]), 128);
+            mbar_init(smem_addr(&sm.p_full[s]), 128);
+            mbar_init(smem_addr(&sm.p_free[s]), 1);
+            mbar_init(smem_addr(&sm.o_free[s]), 128);
+            mbar_init(smem_addr(&sm.drain[s]), 1);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sm.wsum[w];
+        total += sm.wsum[w];
+    }
+    const long long ctas = min(static_cast<long long>(gridDim.x), total);
+    if (blockIdx.x >= ctas) return;
+    const long long at = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+    if (before <= at && at < before + mine) {
+        long long b = before;
+        for (long long i = ia; i < ib; ++i) {
+            const long long n = units(i);
+            if (at < b + n) {
+                sm.start_item = i;
+                sm.start_before = b;
+                break;
+            }
+            b += n;
+        }
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&sm.tmem_base), TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    Walk walk;
+    items.load(walk, sm.start_item, at - sm.start_before, end - at);
+    bool running = walk.c0 < walk.c1 || items.next(walk);
+
+    if (warp < 4) {
+        reg_dec<ROLE_REGS>();
+        if (warp == 0) {
+            // ==================================================== loader ====
+            const int piece_rows = min(B, BN);
+            const int pieces = BN / piece_rows;
+            const uint32_t piece_bytes = static_cast<uint32_t>(piece_rows) * HD;
+            const int group_piece = lane * 16 / piece_rows;    // lanes 0..7: 16-key group -> piece
+            long long n = 0;                                   // tiles so far
+            bool ok = true;
+            float ks = 0.f, vs = 0.f;
+            auto put_scales = [&](long long t) -> bool {       // of tile t, read one tile ago
+                const int s = static_cast<int>(t % SC);
+                if (!mbar_wait_warp(smem_addr(&sm.sc_empty[s]), static_cast<uint32_t>(((t / SC) & 1) ^ 1), wc)) return false;
+                const bool bad = !(fabsf(vs) <= 3.4e38f);
+                // codes under a zero scale are zeros: any scale does, and 1 keeps -inf * s_k what it is.
+                // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
+                const float v = bad || vs == 0.f ? 1.f : fmaxf(vs, 0x1p-100f);
+                const float lv = log2f(v);
+                if (lane < 8) sm.sc[s][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
+                const uint32_t nan = __ballot_sync(0xffffffffu, lane < 8 && bad);
+                if (lane == 0) sm.sc_nan[s] = nan;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
+                return true;
+            };
+            for (; running && ok; running = items.next(walk)) {
+                for (int t = walk.c0; t < walk.c1; ++t, ++n) {
+                    const int s = static_cast<int>(n % RAW);
+                    const long long key0 = static_cast<long long>(t) * BN;
+                    const int have = static_cast<int>((min(walk.len - key0, static_cast<long long>(BN)) + piece_rows - 1) /
+                                                      piece_rows);
+                    int slot = 0;
+                    if (lane < have) slot = slot_of(c, walk.h, (key0 + lane * piece_rows) >> shift, a.status);
+                    if (n > 0 && !(ok = put_scales(n - 1))) break;
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_empty[s]), static_cast<uint32_t>(((n / RAW) & 1) ^ 1), wc))) break;
+                    const uint32_t bar = smem_addr(&sm.raw_full[s]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have) * 2 * piece_bytes);
+                    __syncwarp();
+                    const long long blk = static_cast<long long>(walk.h) * c.slots + slot;
+                    if (lane < have) {
+                        const long long byte = (blk * B + ((key0 + lane * piece_rows) & (B - 1))) * HD;
+                        bulk_load(smem_addr(&sm.raw[s][0][lane * piece_bytes]), c.k + byte, piece_bytes, bar);
+                        bulk_load(smem_addr(&sm.raw[s][1][lane * piece_bytes]), c.v + byte, piece_bytes, bar);
+                    }
+                    const long long gblk = __shfl_sync(0xffffffffu, blk, group_piece & 31);
+                    ks = vs = 0.f;
+                    if (lane < 8 && group_piece < have) {
+                        ks = __ldg(c.k_scale + gblk);
+                        vs = __ldg(c.v_scale + gblk);
+                    }
+                }
+            }
+            if (ok && n > 0) put_scales(n - 1);
+            // copies in flight still write the ring
+            volatile int no_abort = 0;
+            const WaitCtx w2{a.status, &no_abort, drain_timeout_ns(a.timeout_ns)};
+            for (long long t = n > RAW ? n - RAW : 0; t < n; ++t)
+                mbar_wait(smem_addr(&sm.raw_full[t % RAW]), static_cast<uint32_t>((t / RAW) & 1), w2);
+            (void)pieces;
+        } else if (warp < 3) {
+            // ================================================ MMA issuer ====
+            const int s = warp - 1;
+            if (lane == 0) {
+                constexpr uint32_t IDESC_QK = idesc_f16(BM, BN, 0), IDESC_PV = idesc_f16(BM, HD, 1);
+                const uint32_t s_tmem = tmem + s * SLOT_COLS + TM_S, p_tmem = tmem + s * SLOT_COLS + TM_P;
+                const uint32_t o_tmem = tmem + s * SLOT_COLS + TM_O;
+                long long base = 0;        // tiles of earlier parts
+                uint32_t g = 0, part = 0;  // this slot's steps and parts so far
+                bool ok = true;
+                constexpr int STEP = PAIR ? 1 : 2;
+                for (; running && ok; running = items.next(walk)) {
+                    const int n = walk.c1 - walk.c0;
+                    const int j0 = PAIR ? 0 : s;
+                    if (j0 < n) {
+                        if (!(ok = mbar_wait_sleep(smem_addr(&sm.q_full[s]), part & 1, wc, SLEEP_NS))) break;
+                        auto issue_qk = [&](int j, uint32_t step) -> bool {
+                            const long long t = base + j;
+                            const int st = static_cast<int>(t % K16);
+                            if (!mbar_wait_sleep(smem_addr(&sm.k_full[st]), static_cast<uint32_t>((t / K16) & 1), wc, SLEEP_NS)) return false;
+                            if (!mbar_wait_sleep(smem_addr(&sm.s_free[s]), (step & 1) ^ 1, wc, SLEEP_NS)) return false;
+                            tc_fence_after();
+                            const uint64_t qd = sdesc_sw128(smem_addr(sm.q[s]), 16, 1024);
+                            const uint64_t kd = sdesc_sw128(smem_addr(sm.k16[st]), 16, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < HD / 16; ++kk) umma_ss(s_tmem, qd + kk * 2, kd + kk * 2, IDESC_QK, kk > 0 ? 1u : 0u);
+                            umma_commit(smem_addr(&sm.s_full[s]));
+                            umma_commit(smem_addr(&sm.k_empty[st]));
+                            return true;
+                        };
+                        if (!(ok = issue_qk(j0, g))) break;
+                        for (int j = j0; j < n; j += STEP, ++g) {
+                            if (j + STEP < n && !(ok = issue_qk(j + STEP, g + 1))) break;
+                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.p_full[s]), g & 1, wc, SLEEP_NS))) break;
+                            if (j == j0 && !(ok = mbar_wait_sleep(smem_addr(&sm.o_free[s]), (part & 1) ^ 1, wc, SLEEP_NS))) break;
+                            const long long t = base + j;
+                            const int st = static_cast<int>(t % V16);
+                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.v_full[st]), static_cast<uint32_t>((t / V16) & 1), wc, SLEEP_NS))) break;
+                            tc_fence_after();
+                            const uint64_t vd = sdesc_sw128(smem_addr(sm.v16[st]), 0, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                umma_ts(o_tmem, p_tmem + kk * 8, vd + kk * 128, IDESC_PV, (j > j0 || kk > 0) ? 1u : 0u);
+                            umma_commit(smem_addr(&sm.v_empty[st]));
+                            umma_commit(smem_addr(&sm.p_free[s]));
+                        }
+                        ++part;
+                    }
+                    base += n;
+                }
+                // no MMA of this thread may still run when TMEM is released
+                umma_commit(smem_addr(&sm.drain[s]));
+                volatile int no_abort = 0;
+                const WaitCtx w2{a.status, &no_abort, drain_timeout_ns(a.timeout_ns)};
+                mbar_wait(smem_addr(&sm.drain[s]), 0, w2);
+            }
+        } else if (lane == 0) {
+            // where the join finds the partial results of the items that begin in this run:
+            // this CTA's place and how many CTAs hold parts, 0 for an item held whole
+            for (int part = 0; running; running = items.next(walk), ++part) {
+                if (walk.c0 != 0) continue;
+                // the part's first tile and the item's last one, in units of all items
+                const long long first = end - walk.left - (walk.c1 - walk.c0);
+                const long long to = ((first + walk.nc) * ctas - 1) / total;
+                a.item[walk.item] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
+                                              walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        reg_dec<CONVERT_REGS>();
+        // ================================================== converters ====
+        const int half = warp & 1, which = (warp >> 1) & 1;   // rows 64 half .., 0: K, 1: V
+        const int rot = lane >> 2, piece = lane & 3;          // row within 8, 16-byte piece of it
+        long long n = 0;
+        bool ok = true;
+        for (; running && ok; running = items.next(walk)) {
+            for (int t = walk.c0; t < walk.c1; ++t, ++n) {
+                const int rs = static_cast<int>(n % RAW), st = static_cast<int>(n % (which ? V16 : K16));
+                const uint32_t ph = static_cast<uint32_t>((n / (which ? V16 : K16)) & 1);
+                if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_full[rs]), static_cast<uint32_t>((n / RAW) & 1), wc))) break;
+                const uint8_t* src = sm.raw[rs][which];
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = *reinterpret_cast<const uint4*>(src + (half * 64 + i * 8 + rot) * HD + piece * 16);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[rs]));
+                if (!(ok = mbar_wait_warp(smem_addr(which ? &sm.v_empty[st] : &sm.k_empty[st]), ph ^ 1, wc))) break;
+                uint8_t* dst = which ? sm.v16[st] : sm.k16[st];
+                // values behind the last token must be finite: what the ring holds there is anything
+                const int valid = which ? static_cast<int>(min(walk.len - static_cast<long long>(t) * BN, static_cast<long long>(BN))) : BN;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = half * 64 + i * 8 + rot;
+                    uint32_t o[8];
+                    unpack4<FMT>(w[i].x, o[0], o[1]);
+                    unpack4<FMT>(w[i].y, o[2], o[3]);
+                    unpack4<FMT>(w[i].z, o[4], o[5]);
+                    unpack4<FMT>(w[i].w, o[6], o[7]);
+                    if (row >= valid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = 0u;
+                    }
+                    *reinterpret_cast<uint4*>(dst + row * 128 + ((2 * piece) ^ rot) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + row * 128 + ((2 * piece + 1) ^ rot) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(which ? &sm.v_full[st] : &sm.k_full[st]));
+            }
+        }
+    } else {
+        reg_inc<SOFTMAX_REGS>();
+        // ========================================= softmax of a slot ====
+        const int s = (warp >> 2) - 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tm_s = tmem + lanes + s * SLOT_COLS + TM_S;
+        const uint32_t tm_p = tmem + lanes + s * SLOT_COLS + TM_P;
+        const uint32_t tm_o = tmem + lanes + s * SLOT_COLS + TM_O;
+        const int per_sum = min(B, CHUNK) / 16;                // 16-key groups to a weight sum
+        long long base = 0;
+        uint32_t g = 0, part = 0;
+        bool ok = true;
+        constexpr int STEP = PAIR ? 1 : 2;
+        for (; running && ok; running = items.next(walk), ++part) {
+            const int n = walk.c1 - walk.c0;
+            const int j0 = PAIR ? 0 : s;
+            const long long r_head = static_cast<long long>(walk.tile) * Items<PAIR>::ROWS + (PAIR ? s * BM : 0) + row;
+            const bool live = r_head < a.rows;
+            const long long out_row = static_cast<long long>(walk.h) * a.rows + r_head;
+            float m = -INFINITY, l = 0.f;
+            bool nan_value = false;
+            if (j0 < n) {
+                // Q: the row's largest to [2^14, 2^15), as in kv8_attn.cu.  All of the slot's earlier
+                // Q K^T are done (their S has been read), so its tile is free.
+                float qf;
+                {
+                    uint32_t top = 0;
+                    const uint4* src = reinterpret_cast<const uint4*>(a.Q + out_row * HD);
+                    uint4 w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        w[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                                     __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+                    }
+                    top = max(top << 16, top & 0x7FFF0000u);
+                    const bool finite = top < 0x7F800000u;
+                    const int e = max(static_cast<int>(top >> 23) - 127, -100);
+                    const float up = finite ? __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23) : 0.f;
+                    qf = finite ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * a.scale_log2
+                                : __uint_as_float(0x7FC00000u);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] = finite ? pack_f16x2(bf16_lo(ww[k]) * up, bf16_hi(ww[k]) * up) : 0u;
+                        *reinterpret_cast<uint4*>(sm.q[s] + row * 128 + (i ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_addr(&sm.q_full[s]));
+                }
+                const long long lim = a.causal ? walk.len - a.n_q + 1 + r_head % a.n_q : walk.len;
+                for (int j = j0; j < n; j += STEP, ++g) {
+                    const long long t = base + j;
+                    const int sc = static_cast<int>(t % SC);
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.s_full[s]), g & 1, wc))) break;
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.sc_full[sc]), static_cast<uint32_t>((t / SC) & 1), wc))) break;
+                    tc_fence_after();
+                    float x[BN];
+                    {
+                        uint32_t raw[BN];
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) tmem_ld32(tm_s + i * 32, sub32(raw, i * 32));
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_dep(sub32(raw, i * 32));
+#pragma unroll
+                        for (int e = 0; e < BN; ++e) x[e] = __uint_as_float(raw[e]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(smem_addr(&sm.s_free[s]));
+                    const long long key0 = static_cast<long long>(walk.c0 + j) * BN;
+                    const int seen = static_cast<int>(max(min(lim - key0, static_cast<long long>(BN)), 0ll));
+                    const bool edge = __any_sync(0xffffffffu, seen < BN);
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < BN; ++e)
+                            if (e >= seen) x[e] = -INFINITY;
+                    }
+                    // logits are x f; 16 columns to a scale
+                    float f[8], lv[8];
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 w = sm.sc[sc][q];
+                        f[q] = w.x * qf;
+                        f[q] = f[q] < 1e-37f ? 1e-37f : f[q];        // -inf stays -inf; NaN stays
+                        lv[q] = w.y;
+                        if (edge && q * 16 >= seen) f[q] = 1.f;      // nothing seen: whatever the scale is
+                        float v = fmax3(x[16 * q], x[16 * q + 1], x[16 * q + 2]);
+#pragma unroll
+                        for (int e = 3; e < 15; e += 2) v = fmax3(v, x[16 * q + e], x[16 * q + e + 1]);
+                        mx = fmaxf(mx, fmaf(fmaxf(v, x[16 * q + 15]), f[q], lv[q]));
+                    }
+                    if (const uint32_t bad = sm.sc_nan[sc]; bad) nan_value |= (bad & ((1u << ((seen + 15) >> 4)) - 1u)) != 0;
+                    const bool raise = mx > m + RAISE || (m == -INFINITY && mx > m);
+                    float alpha = 1.f;
+                    if (raise) {
+                        alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+                        m = mx;
+                        l *= alpha;
+                    }
+                    const float nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
+                    uint32_t pk[BN / 2];
+                    float sum16[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint64_t f2 = f2_pack(f[q], f[q]);
+                        const float add = nm + lv[q];
+                        const uint64_t add2 = f2_pack(add, add);
+                        uint64_t acc = 0ull;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float a0, a1;
+                            f2_unpack(f2_fma(f2_pack(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]), f2, add2), a0, a1);
+                            a0 = ex2(a0);
+                            a1 = ex2(a1);
+                            acc = f2_add(acc, f2_pack(a0, a1));
+                            pk[8 * q + e] = pack_f16x2(a0, a1);
+                        }
+                        float s0, s1;
+                        f2_unpack(acc, s0, s1);
+                        sum16[q] = (s0 + s1) * sm.sc[sc][q].z;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
+                    l += ((sum16[0] + sum16[1]) + (sum16[2] + sum16[3])) + ((sum16[4] + sum16[5]) + (sum16[6] + sum16[7]));
+                    if (a.groups) {
+                        // log2 of the sums of each 16, 32 or 64 keys
+                        const long long grp0 = static_cast<long long>(walk.c0 + j) * (8 / per_sum);
+                        float* dst = a.gsum + (static_cast<long long>(walk.h) * a.groups + grp0) * a.rows + r_head;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (per_sum > 1 && (q & 1)) continue;
+                            if (per_sum > 2 && (q & 2)) continue;
+                            float v = sum16[q];
+                            if (per_sum > 1) v += sum16[q | 1];
+                            if (per_sum > 2) v += sum16[q | 2] + sum16[q | 3];
+                            const int k = q / per_sum;
+                            if (live && grp0 + k < a.groups) dst[static_cast<long long>(k) * a.rows] = __log2f(v) - nm;
+                        }
+                    }
+                    // P is free once P V of the step before is done; O then holds every earlier step
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, raise && j > j0)) {
+                        const float al = raise && j > j0 ? alpha : 1.f;
+#pragma unroll 1
+                        for (int i = 0; i < HD / 32; ++i) {
+                            uint32_t ro[32];
+                            tmem_ld32(tm_o + i * 32, ro);
+                            tmem_wait_ld_dep(ro);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * al);
+                            tmem_st32(tm_o + i * 32, ro);
+                            tmem_wait_st();
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i) tmem_st16(tm_p + i * 16, pk + i * 16);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(smem_addr(&sm.p_full[s]));
+                }
+                if (!ok) break;
+                // the last P V
+                if (!(ok = mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
+                tc_fence_after();
+            }
+            base += n;
+            // ---- the part's result ------------------------------------------
+            float o[HD];
+            if (j0 < n) {
+                uint32_t ro[HD];
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) tmem_ld32(tm_o + i * 32, sub32(ro, i * 32));
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) tmem_wait_ld_dep(sub32(ro, i * 32));
+#pragma unroll
+                for (int e = 0; e < HD; ++e) o[e] = __uint_as_float(ro[e]);
+                tc_fence_before();
+                mbar_arrive(smem_addr(&sm.o_free[s]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < HD; ++e) o[e] = 0.f;
+            }
+            if (nan_value) {
+#pragma unroll
+                for (int e = 0; e < HD; ++e) o[e] = __uint_as_float(0x7FC00000u);
+            }
+            if (!PAIR) {
+                // the slots hold the same rows: slot 1 hands its sums to slot 0
+                if (s == 1) {
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.other_empty), (part & 1) ^ 1, wc))) break;
+#pragma unroll
+                    for (int i = 0; i < HD / 4; ++i)
+                        sm.other[i][row] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    sm.other_ml[row] = make_float2(m, l);
+                    mbar_arrive(smem_addr(&sm.other_full));
+                    continue;
+                }
+                if (!(ok = mbar_wait_warp(smem_addr(&sm.other_full), part & 1, wc))) break;
+                const float2 ml = sm.other_ml[row];
+                const float M = fmaxf(m, ml.x);
+                const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                m = M;
+                l = l * f0 + ml.y * f1;
+#pragma unroll
+                for (int i = 0; i < HD / 4; ++i) {
+                    const float4 w = sm.other[i][row];
+                    o[4 * i] = o[4 * i] * f0 + w.x * f1;
+                    o[4 * i + 1] = o[4 * i + 1] * f0 + w.y * f1;
+                    o[4 * i + 2] = o[4 * i + 2] * f0 + w.z * f1;
+                    o[4 * i + 3] = o[4 * i + 3] * f0 + w.w * f1;
+                }
+                mbar_arrive(smem_addr(&sm.other_empty));
+            }
+            if (!live) continue;
+            if (walk.c0 == 0 && walk.c1 == walk.nc) {          // the whole item: the outputs themselves
+                const float inv = l == 0.f ? 0.f : 1.f / l;    // no key: zeros; NaN stays
+                uint4* out = reinterpret_cast<uint4*>(a.O + out_row * HD);
+#pragma unroll
+                for (int i = 0; i < HD / 8; ++i)
+                    out[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                        pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                        pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                        pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                const float total2 = l == 0.f ? -INFINITY : m - SHIFT + log2f(l);
+                if (a.lse) a.lse[out_row] = total2 * LN2;
+                if (a.lse2) a.lse2[out_row] = total2;
+            } else {
+                const long long place = (static_cast<long long>(blockIdx.x) * 2 + (part > 0 ? 1 : 0)) * (PAIR ? 2 : 1) + (PAIR ? s : 0);
+                float4* dst = reinterpret_cast<float4*>(a.part_o + (place * BM + row) * HD);
+#pragma unroll
+                for (int i = 0; i < HD / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                a.part_ml[place * BM + row] = make_float2(m, l);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// The parts of items that several CTAs hold, added up, a CTA for 128 rows; rows of
+// items without a tile become zeros and -inf.  16 threads a row, 4 features each.
+template <bool PAIR>
+__global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
+    wait_for_previous();
+    let_next_start();
+    const int per_item = PAIR ? 2 : 1, row_tiles = a.tiles * per_item;
+    const int h = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, s = PAIR ? rt & 1 : 0;
+    const long long item = static_cast<long long>(h) * a.tiles + rt / per_item;
+    const long long len = head_len(a.lens, h, static_cast<long long>(a.c.slots) * a.c.block);
+    const bool none = item_tiles(a, len, rt / per_item, BM * per_item) == 0;
+    const int2 it = none ? make_int2(0, 0) : a.item[item];
+    if (!none && it.y == 0) return;                  // written whole
+    const int q = threadIdx.x & 15;
+    for (int r = threadIdx.x >> 4; r < BM; r += 16) {
+        const long long r_head = static_cast<long long>(rt) * BM + r;
+        if (r_head >= a.rows) break;
+        auto at = [&](int i) {                       // the i-th CTA's place: its first part, but for the item's own start
+            const long long place = i == 0 ? it.x : (it.x / 2 + i) * 2;
+            return (place * per_item + s) * BM + r;
+        };
+        float M = -INFINITY, L = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[at(i)].x);
+#pragma unroll 2
+        for (int i = 0; i < it.y; ++i) {
+            const float2 ml = a.part_ml[at(i)];
+            const float4 v = reinterpret_cast<const float4*>(a.part_o + at(i) * HD)[q];
+            if (ml.y == 0.f) continue;
+            const float f = ex2(ml.x - M);
+            L = fmaf(ml.y, f, L);
+            sum.x = fmaf(v.x, f, sum.x);
+            sum.y = fmaf(v.y, f, sum.y);
+            sum.z = fmaf(v.z, f, sum.z);
+            sum.w = fmaf(v.w, f, sum.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float total2 = L == 0.f ? -INFINITY : M - SHIFT + log2f(L);
+        const long long row = static_cast<long long>(h) * a.rows + r_head;
+        reinterpret_cast<uint2*>(a.O + row * HD)[q] =
+            make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+        if (q == 0) {
+            if (a.lse) a.lse[row] = total2 * LN2;
+            if (a.lse2) a.lse2[row] = total2;
+        }
+    }
+}
+
+template <int FMT, bool PAIR>
+zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
+    auto* fn = tile_kernel<FMT, PAIR>;
+    constexpr int bytes = sizeof(TileSmem) + 1024;
+    static std::atomic<unsigned long long> done{0};  // devices that have the attribute set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ZB_ERR_CUDA;
+    if (!(done.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return ZB_ERR_CUDA;
+        done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    fn<<<ctas, THREADS, bytes, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
+    const long long blocks = static_cast<long long>(a.c.heads) * a.tiles * (PAIR ? 2 : 1);
+    return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(blocks)), 256, st, a);
+}
+
+}  // namespace
+
+zb_status launch_tiles(const AttnArgs& a, bool pair, int ctas, cudaStream_t st) {
+    if (a.c.format == ZB_KV8_INT8)
+        return pair ? launch<ZB_KV8_INT8, true>(a, ctas, st) : launch<ZB_KV8_INT8, false>(a, ctas, st);
+    return pair ? launch<ZB_KV8_E4M3, true>(a, ctas, st) : launch<ZB_KV8_E4M3, false>(a, ctas, st);
+}
+
+}  // namespace kv8
+}  // namespace zb

@@ -249,7 +249,8 @@ def test_attention_short_lengths(fmt, block, G, n_q, causal):
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("block", [16, 64, 128])
 @pytest.mark.parametrize("lens,G,n_q,causal", [([5000, 3, 2049], 4, 1, False), ([9999], 1, 2, True),
-                                               ([1, 0, 0, 12000, 700], 5, 4, True), ([2100, 300], 2, 150, True)])
+                                               ([1, 0, 0, 12000, 700], 5, 4, True), ([2100, 300], 2, 150, True), ([700, 129, 0, 2], 1, 300, True),
+                                               ([1030, 40], 3, 130, False), ([3000], 4, 32, True)])
 def test_attention_long_lengths(fmt, block, lens, G, n_q, causal):
     import linear_hybrid_attention_b200 as zb
     c, ora = _filled(zb, lens, max(lens) + 300, block, fmt, 200 + block)
