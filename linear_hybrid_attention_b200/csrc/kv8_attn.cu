@@ -827,6 +827,9 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return ZB_ERR_ALIGN;
     const kv8::Plan p = kv8::plan(cache, heads_q, n_q, add_mass);
+    // items, and a CTA's share of all items' tiles, in 32 bits
+    const long long tiles = static_cast<long long>(cache.slots) * cache.block / 64 + 3;
+    if (p.tiles * cache.heads > (1ll << 30) || p.tiles * cache.heads > (1ll << 37) / tiles) return ZB_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < p.total) return ZB_ERR_WORKSPACE;
     if (!aligned16(ws)) return ZB_ERR_ALIGN;
     DeviceInfo dev;

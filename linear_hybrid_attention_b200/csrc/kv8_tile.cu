@@ -63,7 +63,7 @@ struct __align__(1024) TileSmem {
     uint64_t q_full[2], s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
     unsigned long long wsum[THREADS / 32];
     long long start_before;
-    long long start_item;
+    int start_item;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -89,59 +89,79 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 }
 
 // Tiles of an item: those its last-reaching row sees.
-ZB_DEVINL int item_tiles(const AttnArgs& a, long long len, int tile, int item_rows) {
+ZB_DEVINL int item_tiles(const AttnArgs& a, int len, int tile, int item_rows) {
     if (a.causal) {
-        const long long r0 = static_cast<long long>(tile) * item_rows;
-        const long long r1 = min(r0 + item_rows, static_cast<long long>(a.rows)) - 1;
-        const long long reach = r0 / a.n_q == r1 / a.n_q ? r1 % a.n_q : a.n_q - 1;
-        len = min(len, max(len - a.n_q + 1 + reach, 0ll));
+        const int r0 = tile * item_rows, r1 = min(r0 + item_rows, a.rows) - 1;
+        const int reach = r0 / a.n_q == r1 / a.n_q ? r1 % a.n_q : a.n_q - 1;
+        len = min(len, max(len - a.n_q + 1 + reach, 0));
     }
-    return static_cast<int>((len + BN - 1) / BN);
+    return static_cast<int>((static_cast<unsigned>(len) + BN - 1) / BN);
 }
 
 // Units of an item in the runs: two for its start (Q, and a pipeline that runs
 // empty) and one a tile.
 constexpr int START = 2;
-ZB_DEVINL long long item_units(int tiles) { return tiles ? tiles + START : 0; }
+ZB_DEVINL int item_units(int tiles) { return tiles ? tiles + START : 0; }
 
 // The parts of items that make up a CTA's run, in order; every role walks them.
+// The host refuses calls whose runs could pass 32 bits.
 struct Walk {
-    long long item, left;     // units of the run after this part
-    int h, tile, c0, c1, nc;
-    long long len;
+    int h, tile, len;
+    int c0, c1, nc;           // the part's tiles, the item's
+    int left;                 // units of the run after this part
 };
 
 template <bool PAIR>
 struct Items {
     static constexpr int ROWS = PAIR ? 256 : 128;
     const AttnArgs& a;
-    long long cap;
-    ZB_DEVINL void load(Walk& w, long long item, long long into, long long left) const {
-        w.item = item;
-        w.h = static_cast<int>(item / a.tiles);
-        w.tile = static_cast<int>(item - static_cast<long long>(w.h) * a.tiles);
-        w.len = head_len(a.lens, w.h, cap);
+    int cap;
+    ZB_DEVINL int len(int h) const { return static_cast<int>(head_len(a.lens, h, cap)); }
+    ZB_DEVINL void load(Walk& w, int into, int left) const {
+        w.len = len(w.h);
         w.nc = item_tiles(a, w.len, w.tile, ROWS);
-        const long long here = min(left, item_units(w.nc) - into);
-        w.c0 = max(static_cast<int>(into) - START, 0);
-        w.c1 = max(static_cast<int>(into + here) - START, 0);
+        const int here = min(left, item_units(w.nc) - into);
+        w.c0 = max(into - START, 0);
+        w.c1 = max(into + here - START, 0);
         w.left = left - here;
     }
     // To the next part with a tile in it; false at the run's end.
     ZB_DEVINL bool next(Walk& w) const {
         do {
-            if (w.left == 0) return false;
-            long long item = w.item + 1;
-            while (item_tiles(a, head_len(a.lens, static_cast<int>(item / a.tiles), cap),
-                              static_cast<int>(item % a.tiles), ROWS) == 0)
-                ++item;
-            load(w, item, 0, w.left);
+            if (w.left <= 0) return false;
+            do {
+                if (++w.tile == a.tiles) {
+                    w.tile = 0;
+                    ++w.h;
+                }
+            } while (item_tiles(a, len(w.h), w.tile, ROWS) == 0);
+            load(w, 0, w.left);
         } while (w.c0 >= w.c1);
         return true;
     }
+    ZB_DEVINL long long index(const Walk& w) const { return static_cast<long long>(w.h) * a.tiles + w.tile; }
 };
 
-template <int FMT, bool PAIR>
+// A place in a ring of N stages.
+template <int N>
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    ZB_DEVINL void step() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    ZB_DEVINL void back() {
+        if (--st < 0) {
+            st = N - 1;
+            ph ^= 1u;
+        }
+    }
+};
+
+template <int FMT, bool PAIR, bool MASS>
 __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     let_next_start();
     extern __shared__ uint8_t smem_raw[];
@@ -149,20 +169,17 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     const int warp = warp_id(), lane = lane_id();
     const zb_kv8& c = a.c;
     const int B = c.block, shift = 31 - __clz(B);
-    const long long cap = static_cast<long long>(c.slots) * B;
-    const Items<PAIR> items{a, cap};
+    const Items<PAIR> items{a, c.slots * B};
     const WaitCtx wc{a.status, &sm.abort_flag, a.timeout_ns};
 
     // ---- this CTA's run ------------------------------------------------------
-    const long long n_items = static_cast<long long>(c.heads) * a.tiles;
-    const long long per = (n_items + THREADS - 1) / THREADS;
-    const long long ia = min(threadIdx.x * per, n_items), ib = min(ia + per, n_items);
-    auto units = [&](long long i) {
-        return item_units(item_tiles(a, head_len(a.lens, static_cast<int>(i / a.tiles), cap),
-                                     static_cast<int>(i % a.tiles), Items<PAIR>::ROWS));
-    };
+    const int n_items = c.heads * a.tiles;
+    const int per = (n_items + THREADS - 1) / THREADS;
+    const int ia = static_cast<int>(min(static_cast<long long>(threadIdx.x) * per, static_cast<long long>(n_items)));
+    const int ib = min(ia + per, n_items);
+    auto units = [&](int i) { return item_units(item_tiles(a, items.len(i / a.tiles), i % a.tiles, Items<PAIR>::ROWS)); };
     long long mine = 0;
-    for (long long i = ia; i < ib; ++i) mine += units(i);
+    for (int i = ia; i < ib; ++i) mine += units(i);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -212,8 +229,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     const long long at = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
     if (before <= at && at < before + mine) {
         long long b = before;
-        for (long long i = ia; i < ib; ++i) {
-            const long long n = units(i);
+        for (int i = ia; i < ib; ++i) {
+            const int n = units(i);
             if (at < b + n) {
                 sm.start_item = i;
                 sm.start_before = b;
@@ -228,7 +245,9 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     Walk walk;
-    items.load(walk, sm.start_item, at - sm.start_before, end - at);
+    walk.h = sm.start_item / a.tiles;
+    walk.tile = sm.start_item % a.tiles;
+    items.load(walk, static_cast<int>(at - sm.start_before), static_cast<int>(end - at));
     bool running = walk.c0 < walk.c1 || items.next(walk);
 
     if (warp < 4) {
@@ -236,45 +255,44 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         if (warp == 0) {
             // ==================================================== loader ====
             const int piece_rows = min(B, BN);
-            const int pieces = BN / piece_rows;
             const uint32_t piece_bytes = static_cast<uint32_t>(piece_rows) * HD;
             const int group_piece = lane * 16 / piece_rows;    // lanes 0..7: 16-key group -> piece
-            long long n = 0;                                   // tiles so far
-            bool ok = true;
+            Ring<RAW> raw;
+            Ring<SC> sc;
+            int issued = 0;
+            bool ok = true, held = false;                      // scales read and not yet put
             float ks = 0.f, vs = 0.f;
-            auto put_scales = [&](long long t) -> bool {       // of tile t, read one tile ago
-                const int s = static_cast<int>(t % SC);
-                if (!mbar_wait_warp(smem_addr(&sm.sc_empty[s]), static_cast<uint32_t>(((t / SC) & 1) ^ 1), wc)) return false;
+            auto put_scales = [&]() -> bool {                  // of the tile before
+                if (!mbar_wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc)) return false;
                 const bool bad = !(fabsf(vs) <= 3.4e38f);
                 // codes under a zero scale are zeros: any scale does, and 1 keeps -inf * s_k what it is.
                 // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
                 const float v = bad || vs == 0.f ? 1.f : fmaxf(vs, 0x1p-100f);
                 const float lv = log2f(v);
-                if (lane < 8) sm.sc[s][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
+                if (lane < 8) sm.sc[sc.st][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
                 const uint32_t nan = __ballot_sync(0xffffffffu, lane < 8 && bad);
-                if (lane == 0) sm.sc_nan[s] = nan;
+                if (lane == 0) sm.sc_nan[sc.st] = nan;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
+                if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[sc.st]));
+                sc.step();
                 return true;
             };
             for (; running && ok; running = items.next(walk)) {
-                for (int t = walk.c0; t < walk.c1; ++t, ++n) {
-                    const int s = static_cast<int>(n % RAW);
-                    const long long key0 = static_cast<long long>(t) * BN;
-                    const int have = static_cast<int>((min(walk.len - key0, static_cast<long long>(BN)) + piece_rows - 1) /
-                                                      piece_rows);
+                for (int t = walk.c0; t < walk.c1; ++t) {
+                    const int key0 = t * BN;
+                    const int have = (min(walk.len - key0, BN) + piece_rows - 1) / piece_rows;
                     int slot = 0;
                     if (lane < have) slot = slot_of(c, walk.h, (key0 + lane * piece_rows) >> shift, a.status);
-                    if (n > 0 && !(ok = put_scales(n - 1))) break;
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_empty[s]), static_cast<uint32_t>(((n / RAW) & 1) ^ 1), wc))) break;
-                    const uint32_t bar = smem_addr(&sm.raw_full[s]);
+                    if (held && !(ok = put_scales())) break;
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_empty[raw.st]), raw.ph ^ 1u, wc))) break;
+                    const uint32_t bar = smem_addr(&sm.raw_full[raw.st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have) * 2 * piece_bytes);
                     __syncwarp();
                     const long long blk = static_cast<long long>(walk.h) * c.slots + slot;
                     if (lane < have) {
                         const long long byte = (blk * B + ((key0 + lane * piece_rows) & (B - 1))) * HD;
-                        bulk_load(smem_addr(&sm.raw[s][0][lane * piece_bytes]), c.k + byte, piece_bytes, bar);
-                        bulk_load(smem_addr(&sm.raw[s][1][lane * piece_bytes]), c.v + byte, piece_bytes, bar);
+                        bulk_load(smem_addr(&sm.raw[raw.st][0][lane * piece_bytes]), c.k + byte, piece_bytes, bar);
+                        bulk_load(smem_addr(&sm.raw[raw.st][1][lane * piece_bytes]), c.v + byte, piece_bytes, bar);
                     }
                     const long long gblk = __shfl_sync(0xffffffffu, blk, group_piece & 31);
                     ks = vs = 0.f;
@@ -282,15 +300,19 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         ks = __ldg(c.k_scale + gblk);
                         vs = __ldg(c.v_scale + gblk);
                     }
+                    held = true;
+                    raw.step();
+                    ++issued;
                 }
             }
-            if (ok && n > 0) put_scales(n - 1);
+            if (ok && held) put_scales();
             // copies in flight still write the ring
             volatile int no_abort = 0;
             const WaitCtx w2{a.status, &no_abort, drain_timeout_ns(a.timeout_ns)};
-            for (long long t = n > RAW ? n - RAW : 0; t < n; ++t)
-                mbar_wait(smem_addr(&sm.raw_full[t % RAW]), static_cast<uint32_t>((t / RAW) & 1), w2);
-            (void)pieces;
+            for (int i = 0; i < min(issued, RAW); ++i) {       // back from the newest
+                raw.back();
+                mbar_wait(smem_addr(&sm.raw_full[raw.st]), raw.ph, w2);
+            }
         } else if (warp < 3) {
             // ================================================ MMA issuer ====
             const int s = warp - 1;
@@ -298,48 +320,60 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 constexpr uint32_t IDESC_QK = idesc_f16(BM, BN, 0), IDESC_PV = idesc_f16(BM, HD, 1);
                 const uint32_t s_tmem = tmem + s * SLOT_COLS + TM_S, p_tmem = tmem + s * SLOT_COLS + TM_P;
                 const uint32_t o_tmem = tmem + s * SLOT_COLS + TM_O;
-                long long base = 0;        // tiles of earlier parts
+                Ring<K16> kr;              // this slot's next tile (a slot of its own rows skips the other's)
+                Ring<V16> vr;
                 uint32_t g = 0, part = 0;  // this slot's steps and parts so far
                 bool ok = true;
                 constexpr int STEP = PAIR ? 1 : 2;
+                const uint64_t qd = sdesc_sw128(smem_addr(sm.q[s]), 16, 1024);
                 for (; running && ok; running = items.next(walk)) {
                     const int n = walk.c1 - walk.c0;
                     const int j0 = PAIR ? 0 : s;
+                    if (!PAIR && s) {
+                        kr.step();
+                        vr.step();
+                    }
                     if (j0 < n) {
                         if (!(ok = mbar_wait_sleep(smem_addr(&sm.q_full[s]), part & 1, wc, SLEEP_NS))) break;
-                        auto issue_qk = [&](int j, uint32_t step) -> bool {
-                            const long long t = base + j;
-                            const int st = static_cast<int>(t % K16);
-                            if (!mbar_wait_sleep(smem_addr(&sm.k_full[st]), static_cast<uint32_t>((t / K16) & 1), wc, SLEEP_NS)) return false;
+                        auto issue_qk = [&](uint32_t step) -> bool {
+                            if (!mbar_wait_sleep(smem_addr(&sm.k_full[kr.st]), kr.ph, wc, SLEEP_NS)) return false;
                             if (!mbar_wait_sleep(smem_addr(&sm.s_free[s]), (step & 1) ^ 1, wc, SLEEP_NS)) return false;
                             tc_fence_after();
-                            const uint64_t qd = sdesc_sw128(smem_addr(sm.q[s]), 16, 1024);
-                            const uint64_t kd = sdesc_sw128(smem_addr(sm.k16[st]), 16, 1024);
+                            const uint64_t kd = sdesc_sw128(smem_addr(sm.k16[kr.st]), 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < HD / 16; ++kk) umma_ss(s_tmem, qd + kk * 2, kd + kk * 2, IDESC_QK, kk > 0 ? 1u : 0u);
                             umma_commit(smem_addr(&sm.s_full[s]));
-                            umma_commit(smem_addr(&sm.k_empty[st]));
+                            umma_commit(smem_addr(&sm.k_empty[kr.st]));
+                            kr.step();
+                            if (!PAIR) kr.step();
                             return true;
                         };
-                        if (!(ok = issue_qk(j0, g))) break;
+                        if (!(ok = issue_qk(g))) break;
                         for (int j = j0; j < n; j += STEP, ++g) {
-                            if (j + STEP < n && !(ok = issue_qk(j + STEP, g + 1))) break;
-                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.p_full[s]), g & 1, wc, SLEEP_NS))) break;
+                            if (j + STEP < n && !(ok = issue_qk(g + 1))) break;
+                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.v_full[vr.st]), vr.ph, wc, SLEEP_NS))) break;
                             if (j == j0 && !(ok = mbar_wait_sleep(smem_addr(&sm.o_free[s]), (part & 1) ^ 1, wc, SLEEP_NS))) break;
-                            const long long t = base + j;
-                            const int st = static_cast<int>(t % V16);
-                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.v_full[st]), static_cast<uint32_t>((t / V16) & 1), wc, SLEEP_NS))) break;
+                            if (!(ok = mbar_wait_sleep(smem_addr(&sm.p_full[s]), g & 1, wc, SLEEP_NS))) break;
                             tc_fence_after();
-                            const uint64_t vd = sdesc_sw128(smem_addr(sm.v16[st]), 0, 1024);
+                            const uint64_t vd = sdesc_sw128(smem_addr(sm.v16[vr.st]), 0, 1024);
 #pragma unroll
                             for (int kk = 0; kk < BN / 16; ++kk)
                                 umma_ts(o_tmem, p_tmem + kk * 8, vd + kk * 128, IDESC_PV, (j > j0 || kk > 0) ? 1u : 0u);
-                            umma_commit(smem_addr(&sm.v_empty[st]));
+                            umma_commit(smem_addr(&sm.v_empty[vr.st]));
                             umma_commit(smem_addr(&sm.p_free[s]));
+                            vr.step();
+                            if (!PAIR) vr.step();
                         }
+                        if (!ok) break;
                         ++part;
                     }
-                    base += n;
+                    if (!PAIR) {           // to the next part's first tile (each slot has gone past its last by two)
+                        const int over = j0 < n ? ((n - j0 + 1) / 2) * 2 + j0 - n : j0 - n;
+                        for (int i = 0; i < over; ++i) {
+                            kr.back();
+                            vr.back();
+                        }
+                    }
                 }
                 // no MMA of this thread may still run when TMEM is released
                 umma_commit(smem_addr(&sm.drain[s]));
@@ -355,8 +389,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 // the part's first tile and the item's last one, in units of all items
                 const long long first = end - walk.left - (walk.c1 - walk.c0);
                 const long long to = ((first + walk.nc) * ctas - 1) / total;
-                a.item[walk.item] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
-                                              walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
+                a.item[items.index(walk)] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
+                                                      walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
             }
         }
         __syncwarp();
@@ -365,24 +399,28 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         // ================================================== converters ====
         const int half = warp & 1, which = (warp >> 1) & 1;   // rows 64 half .., 0: K, 1: V
         const int rot = lane >> 2, piece = lane & 3;          // row within 8, 16-byte piece of it
-        long long n = 0;
+        static_assert(K16 == V16, "one ring walk for both");
+        Ring<RAW> raw;
+        Ring<K16> to;
+        uint64_t* const full = which ? sm.v_full : sm.k_full;
+        uint64_t* const empty = which ? sm.v_empty : sm.k_empty;
+        uint8_t* const tiles = which ? sm.v16[0] : sm.k16[0];
         bool ok = true;
         for (; running && ok; running = items.next(walk)) {
-            for (int t = walk.c0; t < walk.c1; ++t, ++n) {
-                const int rs = static_cast<int>(n % RAW), st = static_cast<int>(n % (which ? V16 : K16));
-                const uint32_t ph = static_cast<uint32_t>((n / (which ? V16 : K16)) & 1);
-                if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_full[rs]), static_cast<uint32_t>((n / RAW) & 1), wc))) break;
-                const uint8_t* src = sm.raw[rs][which];
+            for (int t = walk.c0; t < walk.c1; ++t) {
+                if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_full[raw.st]), raw.ph, wc))) break;
+                const uint8_t* src = sm.raw[raw.st][which];
                 uint4 w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w[i] = *reinterpret_cast<const uint4*>(src + (half * 64 + i * 8 + rot) * HD + piece * 16);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[rs]));
-                if (!(ok = mbar_wait_warp(smem_addr(which ? &sm.v_empty[st] : &sm.k_empty[st]), ph ^ 1, wc))) break;
-                uint8_t* dst = which ? sm.v16[st] : sm.k16[st];
+                if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[raw.st]));
+                raw.step();
+                if (!(ok = mbar_wait_warp(smem_addr(empty + to.st), to.ph ^ 1u, wc))) break;
+                uint8_t* dst = tiles + to.st * TILE_BYTES;
                 // values behind the last token must be finite: what the ring holds there is anything
-                const int valid = which ? static_cast<int>(min(walk.len - static_cast<long long>(t) * BN, static_cast<long long>(BN))) : BN;
+                const int valid = which ? min(walk.len - t * BN, BN) : BN;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int row = half * 64 + i * 8 + rot;
@@ -400,7 +438,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(which ? &sm.v_full[st] : &sm.k_full[st]));
+                if (lane == 0) mbar_arrive(smem_addr(full + to.st));
+                to.step();
             }
         }
     } else {
@@ -413,14 +452,13 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         const uint32_t tm_p = tmem + lanes + s * SLOT_COLS + TM_P;
         const uint32_t tm_o = tmem + lanes + s * SLOT_COLS + TM_O;
         const int per_sum = min(B, CHUNK) / 16;                // 16-key groups to a weight sum
-        long long base = 0;
-        uint32_t g = 0, part = 0;
+        uint32_t base = 0, g = 0, part = 0;   // tiles of earlier parts; this slot's steps; parts
         bool ok = true;
         constexpr int STEP = PAIR ? 1 : 2;
         for (; running && ok; running = items.next(walk), ++part) {
             const int n = walk.c1 - walk.c0;
             const int j0 = PAIR ? 0 : s;
-            const long long r_head = static_cast<long long>(walk.tile) * Items<PAIR>::ROWS + (PAIR ? s * BM : 0) + row;
+            const int r_head = walk.tile * Items<PAIR>::ROWS + (PAIR ? s * BM : 0) + row;
             const bool live = r_head < a.rows;
             const long long out_row = static_cast<long long>(walk.h) * a.rows + r_head;
             float m = -INFINITY, l = 0.f;
@@ -456,12 +494,16 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     fence_proxy_async_smem();
                     mbar_arrive(smem_addr(&sm.q_full[s]));
                 }
-                const long long lim = a.causal ? walk.len - a.n_q + 1 + r_head % a.n_q : walk.len;
+                const int lim = a.causal ? walk.len - a.n_q + 1 + r_head % a.n_q : walk.len;
+                // weight sums of this part's tiles, in order (SPLIT: every second tile)
+                const int per_tile = 8 / per_sum;
+                int gsum_left = a.groups - (walk.c0 + j0) * per_tile;
+                float* gsum = a.gsum + (static_cast<long long>(walk.h) * a.groups + static_cast<long long>(walk.c0 + j0) * per_tile) * a.rows + r_head;
                 for (int j = j0; j < n; j += STEP, ++g) {
-                    const long long t = base + j;
-                    const int sc = static_cast<int>(t % SC);
+                    const uint32_t t = base + j;
+                    const int sc = t % SC;
                     if (!(ok = mbar_wait_warp(smem_addr(&sm.s_full[s]), g & 1, wc))) break;
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.sc_full[sc]), static_cast<uint32_t>((t / SC) & 1), wc))) break;
+                    if (!(ok = mbar_wait_warp(smem_addr(&sm.sc_full[sc]), (t / SC) & 1, wc))) break;
                     tc_fence_after();
                     float x[BN];
                     {
@@ -475,28 +517,27 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     tc_fence_before();
                     mbar_arrive(smem_addr(&sm.s_free[s]));
-                    const long long key0 = static_cast<long long>(walk.c0 + j) * BN;
-                    const int seen = static_cast<int>(max(min(lim - key0, static_cast<long long>(BN)), 0ll));
+                    const int seen = max(min(lim - (walk.c0 + j) * BN, BN), 0);
                     const bool edge = __any_sync(0xffffffffu, seen < BN);
                     if (edge) {
 #pragma unroll
                         for (int e = 0; e < BN; ++e)
                             if (e >= seen) x[e] = -INFINITY;
                     }
-                    // logits are x f; 16 columns to a scale
-                    float f[8], lv[8];
+                    // logits are x f; 16 columns to a scale (read again below: registers are short)
+                    auto factor = [&](float ks, int q) {
+                        float f = ks * qf;
+                        f = f < 1e-37f ? 1e-37f : f;                 // -inf stays -inf; NaN stays
+                        return edge && q * 16 >= seen ? 1.f : f;     // nothing seen: whatever the scale is
+                    };
                     float mx = -INFINITY;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const float4 w = sm.sc[sc][q];
-                        f[q] = w.x * qf;
-                        f[q] = f[q] < 1e-37f ? 1e-37f : f[q];        // -inf stays -inf; NaN stays
-                        lv[q] = w.y;
-                        if (edge && q * 16 >= seen) f[q] = 1.f;      // nothing seen: whatever the scale is
+                        const float2 w = *reinterpret_cast<const float2*>(&sm.sc[sc][q]);
                         float v = fmax3(x[16 * q], x[16 * q + 1], x[16 * q + 2]);
 #pragma unroll
                         for (int e = 3; e < 15; e += 2) v = fmax3(v, x[16 * q + e], x[16 * q + e + 1]);
-                        mx = fmaxf(mx, fmaf(fmaxf(v, x[16 * q + 15]), f[q], lv[q]));
+                        mx = fmaxf(mx, fmaf(fmaxf(v, x[16 * q + 15]), factor(w.x, q), w.y));
                     }
                     if (const uint32_t bad = sm.sc_nan[sc]; bad) nan_value |= (bad & ((1u << ((seen + 15) >> 4)) - 1u)) != 0;
                     const bool raise = mx > m + RAISE || (m == -INFINITY && mx > m);
@@ -508,12 +549,13 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     const float nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
                     uint32_t pk[BN / 2];
+                    float weight = 0.f;                              // of a run of per_sum groups
                     float sum16[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const uint64_t f2 = f2_pack(f[q], f[q]);
-                        const float add = nm + lv[q];
-                        const uint64_t add2 = f2_pack(add, add);
+                        const float4 w = sm.sc[sc][q];
+                        const float f = factor(w.x, q), add = nm + w.y;
+                        const uint64_t f2 = f2_pack(f, f), add2 = f2_pack(add, add);
                         uint64_t acc = 0ull;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -526,26 +568,21 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         }
                         float s0, s1;
                         f2_unpack(acc, s0, s1);
-                        sum16[q] = (s0 + s1) * sm.sc[sc][q].z;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
-                    l += ((sum16[0] + sum16[1]) + (sum16[2] + sum16[3])) + ((sum16[4] + sum16[5]) + (sum16[6] + sum16[7]));
-                    if (a.groups) {
-                        // log2 of the sums of each 16, 32 or 64 keys
-                        const long long grp0 = static_cast<long long>(walk.c0 + j) * (8 / per_sum);
-                        float* dst = a.gsum + (static_cast<long long>(walk.h) * a.groups + grp0) * a.rows + r_head;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (per_sum > 1 && (q & 1)) continue;
-                            if (per_sum > 2 && (q & 2)) continue;
-                            float v = sum16[q];
-                            if (per_sum > 1) v += sum16[q | 1];
-                            if (per_sum > 2) v += sum16[q | 2] + sum16[q | 3];
-                            const int k = q / per_sum;
-                            if (live && grp0 + k < a.groups) dst[static_cast<long long>(k) * a.rows] = __log2f(v) - nm;
+                        sum16[q] = (s0 + s1) * w.z;
+                        if (MASS) {
+                            // log2 of the sums of each 16, 32 or 64 keys
+                            weight += sum16[q];
+                            if (((q + 1) & (per_sum - 1)) == 0) {
+                                if (live && gsum_left > 0) *gsum = __log2f(weight) - nm;
+                                gsum += a.rows;
+                                --gsum_left;
+                                weight = 0.f;
+                            }
                         }
                     }
+                    l += ((sum16[0] + sum16[1]) + (sum16[2] + sum16[3])) + ((sum16[4] + sum16[5]) + (sum16[6] + sum16[7]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
                     // P is free once P V of the step before is done; O then holds every earlier step
                     if (!(ok = mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
                     tc_fence_after();
@@ -567,6 +604,10 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(smem_addr(&sm.p_full[s]));
+                    if (!PAIR && MASS) {                         // the other slot's tile
+                        gsum += static_cast<long long>(per_tile) * a.rows;
+                        gsum_left -= per_tile;
+                    }
                 }
                 if (!ok) break;
                 // the last P V
@@ -660,7 +701,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
     const int per_item = PAIR ? 2 : 1, row_tiles = a.tiles * per_item;
     const int h = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, s = PAIR ? rt & 1 : 0;
     const long long item = static_cast<long long>(h) * a.tiles + rt / per_item;
-    const long long len = head_len(a.lens, h, static_cast<long long>(a.c.slots) * a.c.block);
+    const int len = static_cast<int>(head_len(a.lens, h, static_cast<long long>(a.c.slots) * a.c.block));
     const bool none = item_tiles(a, len, rt / per_item, BM * per_item) == 0;
     const int2 it = none ? make_int2(0, 0) : a.item[item];
     if (!none && it.y == 0) return;                  // written whole
@@ -699,9 +740,9 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
     }
 }
 
-template <int FMT, bool PAIR>
-zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
-    auto* fn = tile_kernel<FMT, PAIR>;
+template <int FMT, bool PAIR, bool MASS>
+zb_status launch_one(const AttnArgs& a, int ctas, cudaStream_t st) {
+    auto* fn = tile_kernel<FMT, PAIR, MASS>;
     constexpr int bytes = sizeof(TileSmem) + 1024;
     static std::atomic<unsigned long long> done{0};  // devices that have the attribute set
     int dev = 0;
@@ -711,9 +752,15 @@ zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
         done.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     fn<<<ctas, THREADS, bytes, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
-    const long long blocks = static_cast<long long>(a.c.heads) * a.tiles * (PAIR ? 2 : 1);
-    return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(blocks)), 256, st, a);
+    return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}
+
+template <int FMT, bool PAIR>
+zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
+    const zb_status e = a.groups ? launch_one<FMT, PAIR, true>(a, ctas, st) : launch_one<FMT, PAIR, false>(a, ctas, st);
+    if (e != ZB_OK) return e;
+    return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(a.c.heads * a.tiles * (PAIR ? 2 : 1))), 256,
+                         st, a);
 }
 
 }  // namespace
