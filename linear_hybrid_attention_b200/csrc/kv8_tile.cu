@@ -18,9 +18,9 @@
 // less than an item: those go to the workspace, to the CTA's two places there, and a
 // second kernel adds them up.
 //
-// Scales.  s_k multiplies the logits, per 16 columns.  s_v rides in the exponent:
-// P = 2^(x + log2 s_v - m), so that O += P code needs no further product, and the
-// softmax sum takes each 16 columns' sum of P times 1 / s_v.  The running reference
+// Scales.  s_k multiplies the logits, 64 or 16 columns at a time.  s_v rides in the
+// exponent: P = 2^(x + log2 s_v - m), so that O += P code needs no further product,
+// and the softmax sum takes those columns' sum of P times 1 / s_v.  The running reference
 // m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -54,7 +54,7 @@ struct __align__(1024) TileSmem {
     uint8_t raw[RAW][2][RAW_BYTES];
     float4 other[HD / 4][BM];         // slot 1's sums where it shares slot 0's rows
     float2 other_ml[BM];
-    float4 sc[SC][8];                 // s_k, log2 s_v, 1 / s_v of 16 keys
+    float4 sc[SC][8];                 // s_k, log2 s_v, 1 / s_v of 64 or 16 keys
     uint32_t sc_nan[SC];              // bit g: s_v of group g is not finite
     uint64_t raw_full[RAW], raw_empty[RAW];
     uint64_t k_full[K16], k_empty[K16], v_full[V16], v_empty[V16];
@@ -161,7 +161,8 @@ struct Ring {
     }
 };
 
-template <int FMT, bool PAIR, bool MASS>
+// G: scales a tile has (2 for blocks of 64 and 128, 8 for smaller ones).
+template <int FMT, bool PAIR, bool MASS, int G>
 __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     let_next_start();
     extern __shared__ uint8_t smem_raw[];
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             // ==================================================== loader ====
             const int piece_rows = min(B, BN);
             const uint32_t piece_bytes = static_cast<uint32_t>(piece_rows) * HD;
-            const int group_piece = lane * 16 / piece_rows;    // lanes 0..7: 16-key group -> piece
+            const int group_piece = lane * (BN / G) / piece_rows;   // lanes 0..G-1: group of keys -> piece
             Ring<RAW> raw;
             Ring<SC> sc;
             int issued = 0;
@@ -269,8 +270,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
                 const float v = bad || vs == 0.f ? 1.f : fmaxf(vs, 0x1p-100f);
                 const float lv = log2f(v);
-                if (lane < 8) sm.sc[sc.st][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
-                const uint32_t nan = __ballot_sync(0xffffffffu, lane < 8 && bad);
+                if (lane < G) sm.sc[sc.st][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
+                const uint32_t nan = __ballot_sync(0xffffffffu, lane < G && bad);
                 if (lane == 0) sm.sc_nan[sc.st] = nan;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[sc.st]));
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     const long long gblk = __shfl_sync(0xffffffffu, blk, group_piece & 31);
                     ks = vs = 0.f;
-                    if (lane < 8 && group_piece < have) {
+                    if (lane < G && group_piece < have) {
                         ks = __ldg(c.k_scale + gblk);
                         vs = __ldg(c.v_scale + gblk);
                     }
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         const uint32_t tm_s = tmem + lanes + s * SLOT_COLS + TM_S;
         const uint32_t tm_p = tmem + lanes + s * SLOT_COLS + TM_P;
         const uint32_t tm_o = tmem + lanes + s * SLOT_COLS + TM_O;
-        const int per_sum = min(B, CHUNK) / 16;                // 16-key groups to a weight sum
+        const int per_sum = G == 2 ? 1 : B / 16;               // scales to a weight sum
         uint32_t base = 0, g = 0, part = 0;   // tiles of earlier parts; this slot's steps; parts
         bool ok = true;
         constexpr int STEP = PAIR ? 1 : 2;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 }
                 const int lim = a.causal ? walk.len - a.n_q + 1 + r_head % a.n_q : walk.len;
                 // weight sums of this part's tiles, in order (SPLIT: every second tile)
-                const int per_tile = 8 / per_sum;
+                const int per_tile = G / per_sum;
                 int gsum_left = a.groups - (walk.c0 + j0) * per_tile;
                 float* gsum = a.gsum + (static_cast<long long>(walk.h) * a.groups + static_cast<long long>(walk.c0 + j0) * per_tile) * a.rows + r_head;
                 for (int j = j0; j < n; j += STEP, ++g) {
@@ -524,22 +525,32 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         for (int e = 0; e < BN; ++e)
                             if (e >= seen) x[e] = -INFINITY;
                     }
-                    // logits are x f; 16 columns to a scale (read again below: registers are short)
+                    // logits are x f, COLS columns to a scale.  At an edge -inf must stay -inf: f is
+                    // kept off zero, and is 1 where nothing is seen, whatever the scale there is.
+                    constexpr int COLS = BN / G;
                     auto factor = [&](float ks, int q) {
                         float f = ks * qf;
-                        f = f < 1e-37f ? 1e-37f : f;                 // -inf stays -inf; NaN stays
-                        return edge && q * 16 >= seen ? 1.f : f;     // nothing seen: whatever the scale is
+                        if (edge) {
+                            f = f < 1e-37f ? 1e-37f : f;
+                            f = q * COLS >= seen ? 1.f : f;
+                        }
+                        return f;
                     };
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
+                    for (int q = 0; q < G; ++q) {
                         const float2 w = *reinterpret_cast<const float2*>(&sm.sc[sc][q]);
-                        float v = fmax3(x[16 * q], x[16 * q + 1], x[16 * q + 2]);
+                        float v = -INFINITY;
 #pragma unroll
-                        for (int e = 3; e < 15; e += 2) v = fmax3(v, x[16 * q + e], x[16 * q + e + 1]);
-                        mx = fmaxf(mx, fmaf(fmaxf(v, x[16 * q + 15]), factor(w.x, q), w.y));
+                        for (int k = 0; k < COLS; k += 16) {         // a tree of 3-input maxima
+                            float u = fmax3(x[COLS * q + k], x[COLS * q + k + 1], x[COLS * q + k + 2]);
+#pragma unroll
+                            for (int e = 3; e < 15; e += 2) u = fmax3(u, x[COLS * q + k + e], x[COLS * q + k + e + 1]);
+                            v = fmax3(v, u, x[COLS * q + k + 15]);
+                        }
+                        mx = fmaxf(mx, fmaf(v, factor(w.x, q), w.y));
                     }
-                    if (const uint32_t bad = sm.sc_nan[sc]; bad) nan_value |= (bad & ((1u << ((seen + 15) >> 4)) - 1u)) != 0;
+                    if (const uint32_t bad = sm.sc_nan[sc]; bad) nan_value |= (bad & ((1u << ((seen + COLS - 1) / COLS)) - 1u)) != 0;
                     const bool raise = mx > m + RAISE || (m == -INFINITY && mx > m);
                     float alpha = 1.f;
                     if (raise) {
@@ -549,30 +560,31 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     const float nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
                     uint32_t pk[BN / 2];
-                    float weight = 0.f;                              // of a run of per_sum groups
-                    float sum16[8];
+                    float weight = 0.f, add_l = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
+                    for (int q = 0; q < G; ++q) {
                         const float4 w = sm.sc[sc][q];
                         const float f = factor(w.x, q), add = nm + w.y;
                         const uint64_t f2 = f2_pack(f, f), add2 = f2_pack(add, add);
-                        uint64_t acc = 0ull;
+                        uint64_t acc0 = 0ull, acc1 = 0ull;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < COLS / 2; ++e) {
                             float a0, a1;
-                            f2_unpack(f2_fma(f2_pack(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]), f2, add2), a0, a1);
+                            f2_unpack(f2_fma(f2_pack(x[COLS * q + 2 * e], x[COLS * q + 2 * e + 1]), f2, add2), a0, a1);
                             a0 = ex2(a0);
                             a1 = ex2(a1);
-                            acc = f2_add(acc, f2_pack(a0, a1));
-                            pk[8 * q + e] = pack_f16x2(a0, a1);
+                            const uint64_t p2 = f2_pack(a0, a1);
+                            if (e & 1) acc1 = f2_add(acc1, p2); else acc0 = f2_add(acc0, p2);
+                            pk[COLS / 2 * q + e] = pack_f16x2(a0, a1);
                         }
                         float s0, s1;
-                        f2_unpack(acc, s0, s1);
-                        sum16[q] = (s0 + s1) * w.z;
+                        f2_unpack(f2_add(acc0, acc1), s0, s1);
+                        const float sum = (s0 + s1) * w.z;
+                        add_l += sum;
                         if (MASS) {
-                            // log2 of the sums of each 16, 32 or 64 keys
-                            weight += sum16[q];
-                            if (((q + 1) & (per_sum - 1)) == 0) {
+                            // log2 of the sums of each 64 keys, or of a smaller block
+                            weight += sum;
+                            if (G == 2 || ((q + 1) & (per_sum - 1)) == 0) {
                                 if (live && gsum_left > 0) *gsum = __log2f(weight) - nm;
                                 gsum += a.rows;
                                 --gsum_left;
@@ -580,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                             }
                         }
                     }
-                    l += ((sum16[0] + sum16[1]) + (sum16[2] + sum16[3])) + ((sum16[4] + sum16[5]) + (sum16[6] + sum16[7]));
+                    l += add_l;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
                     // P is free once P V of the step before is done; O then holds every earlier step
@@ -740,9 +752,9 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
     }
 }
 
-template <int FMT, bool PAIR, bool MASS>
+template <int FMT, bool PAIR, bool MASS, int G>
 zb_status launch_one(const AttnArgs& a, int ctas, cudaStream_t st) {
-    auto* fn = tile_kernel<FMT, PAIR, MASS>;
+    auto* fn = tile_kernel<FMT, PAIR, MASS, G>;
     constexpr int bytes = sizeof(TileSmem) + 1024;
     static std::atomic<unsigned long long> done{0};  // devices that have the attribute set
     int dev = 0;
@@ -757,7 +769,10 @@ zb_status launch_one(const AttnArgs& a, int ctas, cudaStream_t st) {
 
 template <int FMT, bool PAIR>
 zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
-    const zb_status e = a.groups ? launch_one<FMT, PAIR, true>(a, ctas, st) : launch_one<FMT, PAIR, false>(a, ctas, st);
+    const bool wide = a.c.block >= CHUNK;
+    const zb_status e = a.groups ? wide ? launch_one<FMT, PAIR, true, 2>(a, ctas, st) : launch_one<FMT, PAIR, true, 8>(a, ctas, st)
+                        : wide   ? launch_one<FMT, PAIR, false, 2>(a, ctas, st)
+                                 : launch_one<FMT, PAIR, false, 8>(a, ctas, st);
     if (e != ZB_OK) return e;
     return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(a.c.heads * a.tiles * (PAIR ? 2 : 1))), 256,
                          st, a);
