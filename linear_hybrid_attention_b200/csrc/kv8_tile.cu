@@ -704,51 +704,68 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     }
 }
 
-// The parts of items that several CTAs hold, added up, a CTA for 128 rows; rows of
-// items without a tile become zeros and -inf.  16 threads a row, 4 features each.
+// The parts of items that several CTAs hold, added up; rows of items without a tile
+// become zeros and -inf.  Grid: (row tiles, 8): 16 rows a CTA, 16 threads a row.  A
+// row's thread reads one part's maximum and sum in sixteen and 4 features of all.
 template <bool PAIR>
 __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
-    wait_for_previous();
-    let_next_start();
     const int per_item = PAIR ? 2 : 1, row_tiles = a.tiles * per_item;
     const int h = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles, s = PAIR ? rt & 1 : 0;
-    const long long item = static_cast<long long>(h) * a.tiles + rt / per_item;
     const int len = static_cast<int>(head_len(a.lens, h, static_cast<long long>(a.c.slots) * a.c.block));
     const bool none = item_tiles(a, len, rt / per_item, BM * per_item) == 0;
-    const int2 it = none ? make_int2(0, 0) : a.item[item];
+    wait_for_previous();
+    let_next_start();
+    const int2 it = none ? make_int2(0, 0) : a.item[static_cast<long long>(h) * a.tiles + rt / per_item];
     if (!none && it.y == 0) return;                  // written whole
-    const int q = threadIdx.x & 15;
-    for (int r = threadIdx.x >> 4; r < BM; r += 16) {
-        const long long r_head = static_cast<long long>(rt) * BM + r;
-        if (r_head >= a.rows) break;
-        auto at = [&](int i) {                       // the i-th CTA's place: its first part, but for the item's own start
-            const long long place = i == 0 ? it.x : (it.x / 2 + i) * 2;
-            return (place * per_item + s) * BM + r;
-        };
-        float M = -INFINITY, L = 0.f;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < it.y; ++i) M = fmaxf(M, a.part_ml[at(i)].x);
-#pragma unroll 2
-        for (int i = 0; i < it.y; ++i) {
-            const float2 ml = a.part_ml[at(i)];
-            const float4 v = reinterpret_cast<const float4*>(a.part_o + at(i) * HD)[q];
-            if (ml.y == 0.f) continue;
-            const float f = ex2(ml.x - M);
-            L = fmaf(ml.y, f, L);
-            sum.x = fmaf(v.x, f, sum.x);
-            sum.y = fmaf(v.y, f, sum.y);
-            sum.z = fmaf(v.z, f, sum.z);
-            sum.w = fmaf(v.w, f, sum.w);
+    const int q = threadIdx.x & 15, r = blockIdx.y * 16 + (threadIdx.x >> 4);
+    const int r_head = rt * BM + r;
+    if (r_head >= a.rows) return;                    // (half warps are rows: the shuffles below stay whole)
+    const uint32_t half = 0xFFFFu << (lane_id() & 16);
+    auto at = [&](int i) {                           // the i-th CTA's place: its first part, but for the item's own start
+        const long long place = i == 0 ? it.x : (it.x / 2 + i) * 2;
+        return (place * per_item + s) * BM + r;
+    };
+    float M = -INFINITY, L = 0.f;
+    for (int i = q; i < it.y; i += 16) M = fmaxf(M, a.part_ml[at(i)].x);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < it.y; i0 += 16) {
+        float f = 0.f, l = 0.f;
+        if (i0 + q < it.y) {
+            const float2 ml = a.part_ml[at(i0 + q)];
+            if (ml.y != 0.f) {
+                f = ex2(ml.x - M);
+                l = ml.y * f;
+            }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float total2 = L == 0.f ? -INFINITY : M - SHIFT + log2f(L);
-        const long long row = static_cast<long long>(h) * a.rows + r_head;
-        reinterpret_cast<uint2*>(a.O + row * HD)[q] =
-            make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
-        if (q == 0) {
-            if (a.lse) a.lse[row] = total2 * LN2;
-            if (a.lse2) a.lse2[row] = total2;
+        const int n = min(16, it.y - i0);
+        for (int i1 = 0; i1 < n; i1 += 4) {
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = i1 + k < n ? reinterpret_cast<const float4*>(a.part_o + at(i0 + i1 + k) * HD)[q]
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float fk = __shfl_sync(half, f, (i1 + k) & 15, 16);
+                L += __shfl_sync(half, l, (i1 + k) & 15, 16);   // lanes past the last part hold zeros
+                if (fk == 0.f) continue;
+                sum.x = fmaf(v[k].x, fk, sum.x);
+                sum.y = fmaf(v[k].y, fk, sum.y);
+                sum.z = fmaf(v[k].z, fk, sum.z);
+                sum.w = fmaf(v[k].w, fk, sum.w);
+            }
         }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float total2 = L == 0.f ? -INFINITY : M - SHIFT + log2f(L);
+    const long long row = static_cast<long long>(h) * a.rows + r_head;
+    reinterpret_cast<uint2*>(a.O + row * HD)[q] =
+        make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+    if (q == 0) {
+        if (a.lse) a.lse[row] = total2 * LN2;
+        if (a.lse2) a.lse2[row] = total2;
     }
 }
 
@@ -774,7 +791,7 @@ zb_status launch(const AttnArgs& a, int ctas, cudaStream_t st) {
                         : wide   ? launch_one<FMT, PAIR, false, 2>(a, ctas, st)
                                  : launch_one<FMT, PAIR, false, 8>(a, ctas, st);
     if (e != ZB_OK) return e;
-    return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(a.c.heads * a.tiles * (PAIR ? 2 : 1))), 256,
+    return launch_behind(join_tiles_kernel<PAIR>, dim3(static_cast<unsigned>(a.c.heads * a.tiles * (PAIR ? 2 : 1)), 8), 256,
                          st, a);
 }
 
