@@ -327,9 +327,8 @@ struct EvictArgs {
 // indices among equals, each warp writing its own contiguous part in order.
 // Bound by latency: two dependent gathers (slot, weight), then rounds over a list
 // of some thousand words in shared memory.  256 threads serve lists of up to 2,048
-// blocks, so that several heads share an SM (384 heads of 344 blocks: 13 -> %s us);
-// 1,024 the longer ones (16 heads of 10,992: 16 -> %s us, with E_AHEAD gathers of a
-// thread in flight and the slots kept).
+// blocks, so that several heads share an SM (384 heads of 344 blocks: 13 -> 10.6 us);
+// 1,024 the longer ones (16 heads of 10,992: 15 us).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) evict_kernel(const EvictArgs a) {
     extern __shared__ uint32_t items[];              // keys, then slots

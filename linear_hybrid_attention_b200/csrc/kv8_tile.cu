@@ -5,7 +5,7 @@
 // instructions around them rather than by the cache's bytes.  One persistent CTA
 // per SM, 512 threads:
 //   warp 0        loader: bulk copies of a 128-key tile's codes into a ring, and
-//                 the tile's scales, 16 keys to an entry
+//                 the tile's scales
 //   warps 1, 2    MMA issuers of row tiles ("slots") 0 and 1: S = Q K^T, O += P V
 //   warps 4..7    converters (two for K, two for V): codes to fp16, exactly, in the
 //                 128-byte-swizzle layout the MMAs read
@@ -22,10 +22,20 @@
 // exponent: P = 2^(x + log2 s_v - m), so that O += P code needs no further product,
 // and the softmax sum takes those columns' sum of P times 1 / s_v.  The running reference
 // m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
+//
+// Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
+// tokens: 505 us without weights, 490 TFLOP/s (548 us causal with weights and both
+// joins); 1,280 rows 427 us, 540 TFLOP/s.  A pair of 128 x 128 tiles takes about
+// 3,900 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
+// pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P),
+// which the other slot's warp covers only in part.  Also built, and slower by 2 to
+// 20%: three slots of 64 keys; four slots of 64 keys with P in S's columns; the two
+// slots' exponentials taking turns (a hand-over costs what it saves).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv8.cuh"
 
@@ -41,11 +51,11 @@ constexpr uint32_t TILE_BYTES = BN * HD * 2;       // 16 KB of fp16
 constexpr uint32_t TMEM_COLS = 512, SLOT_COLS = 256, TM_S = 0, TM_P = 128, TM_O = 192;
 constexpr uint32_t SLEEP_NS = 20000;
 // 128 threads each of roles and converters, 256 of softmax; adds up to the launch's 512 x 128
-constexpr int LAUNCH_REGS = 128, ROLE_REGS = 40, CONVERT_REGS = 72, SOFTMAX_REGS = 200;
+constexpr int LAUNCH_REGS = 128, ROLE_REGS = 64, CONVERT_REGS = 96, SOFTMAX_REGS = 176;
 static_assert(128 * (ROLE_REGS + CONVERT_REGS) + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
 // P is at most 2^(SHIFT + RAISE) in fp16 and rounded to 2^-11 of its value down to
 // 2^-(SHIFT + 14) of the reference, to 2^-(SHIFT + 25) of it below.
-constexpr float SHIFT = 11.f, RAISE = 4.f;
+constexpr float SHIFT = 7.f, RAISE = 8.f;
 
 struct __align__(1024) TileSmem {
     uint8_t q[2][TILE_BYTES];
@@ -73,12 +83,28 @@ ZB_DEVINL void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::
 template <int N>
 ZB_DEVINL void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-ZB_DEVINL void tmem_st16(uint32_t taddr, const uint32_t* r) {
+// 32 lanes x consecutive 32-bit columns, moved and waited for in one piece: with the wait
+// apart, tying the registers to it costs a move each.
+ZB_DEVINL void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr), "r"(taddr + 32)
+        : "memory");
+}
+ZB_DEVINL void tmem_store(uint32_t taddr, const uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%1], {%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr), "r"(taddr + 32), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]), "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]), "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]), "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]), "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
+        : "memory");
+}
+ZB_DEVINL void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 
@@ -506,119 +532,117 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     if (!(ok = mbar_wait_warp(smem_addr(&sm.s_full[s]), g & 1, wc))) break;
                     if (!(ok = mbar_wait_warp(smem_addr(&sm.sc_full[sc]), (t / SC) & 1, wc))) break;
                     tc_fence_after();
-                    float x[BN];
-                    {
-                        uint32_t raw[BN];
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_ld32(tm_s + i * 32, sub32(raw, i * 32));
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_dep(sub32(raw, i * 32));
-#pragma unroll
-                        for (int e = 0; e < BN; ++e) x[e] = __uint_as_float(raw[e]);
-                    }
-                    tc_fence_before();
-                    mbar_arrive(smem_addr(&sm.s_free[s]));
                     const int seen = max(min(lim - (walk.c0 + j) * BN, BN), 0);
-                    const bool edge = __any_sync(0xffffffffu, seen < BN);
-                    if (edge) {
+                    float alpha = 1.f, nm = 0.f, weight = 0.f;
+                    bool raise = false;
+                    // A tile is read in halves, the first half twice: for the maximum, and again for its
+                    // exponentials after the second half's.  Held whole, its 128 values left the compiler so
+                    // few registers that it moved each about once more than needed.  Tiles that every row
+                    // sees to their end (all but the last few of an item) get code without a mask.
+                    constexpr int HALF = BN / 2, HG = G / 2, COLS = BN / G;
+                    auto step = [&](auto edge_tag) -> bool {
+                        constexpr bool EDGE = decltype(edge_tag)::value;
+                        auto load = [&](int h, float (&x)[HALF]) {
+                            uint32_t raw[HALF];
+                            tmem_load(tm_s + h * HALF, raw);
 #pragma unroll
-                        for (int e = 0; e < BN; ++e)
-                            if (e >= seen) x[e] = -INFINITY;
-                    }
-                    // logits are x f, COLS columns to a scale.  At an edge -inf must stay -inf: f is
-                    // kept off zero, and is 1 where nothing is seen, whatever the scale there is.
-                    constexpr int COLS = BN / G;
-                    auto factor = [&](float ks, int q) {
-                        float f = ks * qf;
-                        if (edge) {
-                            f = f < 1e-37f ? 1e-37f : f;
-                            f = q * COLS >= seen ? 1.f : f;
-                        }
-                        return f;
-                    };
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < G; ++q) {
-                        const float2 w = *reinterpret_cast<const float2*>(&sm.sc[sc][q]);
-                        float v = -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < COLS; k += 16) {         // a tree of 3-input maxima
-                            float u = fmax3(x[COLS * q + k], x[COLS * q + k + 1], x[COLS * q + k + 2]);
-#pragma unroll
-                            for (int e = 3; e < 15; e += 2) u = fmax3(u, x[COLS * q + k + e], x[COLS * q + k + e + 1]);
-                            v = fmax3(v, u, x[COLS * q + k + 15]);
-                        }
-                        mx = fmaxf(mx, fmaf(v, factor(w.x, q), w.y));
-                    }
-                    if (const uint32_t bad = sm.sc_nan[sc]; bad) nan_value |= (bad & ((1u << ((seen + COLS - 1) / COLS)) - 1u)) != 0;
-                    const bool raise = mx > m + RAISE || (m == -INFINITY && mx > m);
-                    float alpha = 1.f;
-                    if (raise) {
-                        alpha = m == -INFINITY ? 0.f : ex2(m - mx);
-                        m = mx;
-                        l *= alpha;
-                    }
-                    const float nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
-                    uint32_t pk[BN / 2];
-                    float weight = 0.f, add_l = 0.f;
-#pragma unroll
-                    for (int q = 0; q < G; ++q) {
-                        const float4 w = sm.sc[sc][q];
-                        const float f = factor(w.x, q), add = nm + w.y;
-                        const uint64_t f2 = f2_pack(f, f), add2 = f2_pack(add, add);
-                        uint64_t acc0 = 0ull, acc1 = 0ull;
-#pragma unroll
-                        for (int e = 0; e < COLS / 2; ++e) {
-                            float a0, a1;
-                            f2_unpack(f2_fma(f2_pack(x[COLS * q + 2 * e], x[COLS * q + 2 * e + 1]), f2, add2), a0, a1);
-                            a0 = ex2(a0);
-                            a1 = ex2(a1);
-                            const uint64_t p2 = f2_pack(a0, a1);
-                            if (e & 1) acc1 = f2_add(acc1, p2); else acc0 = f2_add(acc0, p2);
-                            pk[COLS / 2 * q + e] = pack_f16x2(a0, a1);
-                        }
-                        float s0, s1;
-                        f2_unpack(f2_add(acc0, acc1), s0, s1);
-                        const float sum = (s0 + s1) * w.z;
-                        add_l += sum;
-                        if (MASS) {
-                            // log2 of the sums of each 64 keys, or of a smaller block
-                            weight += sum;
-                            if (G == 2 || ((q + 1) & (per_sum - 1)) == 0) {
-                                if (live && gsum_left > 0) *gsum = __log2f(weight) - nm;
-                                gsum += a.rows;
-                                --gsum_left;
-                                weight = 0.f;
+                            for (int e = 0; e < HALF; ++e) {
+                                x[e] = __uint_as_float(raw[e]);
+                                if (EDGE) x[e] = h * HALF + e < seen ? x[e] : -INFINITY;
                             }
+                        };
+                        // logits are x f, COLS columns to a scale.  At an edge -inf must stay -inf: f is
+                        // kept off zero, and is 1 where nothing is seen, whatever the scale there is.
+                        auto factor = [&](float ks, int q) {
+                            float f = ks * qf;
+                            if (EDGE) {
+                                f = f < 1e-37f ? 1e-37f : f;
+                                f = q * COLS >= seen ? 1.f : f;
+                            }
+                            return f;
+                        };
+                        auto maximum = [&](int h, const float (&x)[HALF]) {
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int q = 0; q < HG; ++q) {
+                                const float2 w = *reinterpret_cast<const float2*>(&sm.sc[sc][h * HG + q]);
+                                float v = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < COLS; k += 16) { // a tree of 3-input maxima
+                                    float u = fmax3(x[COLS * q + k], x[COLS * q + k + 1], x[COLS * q + k + 2]);
+#pragma unroll
+                                    for (int e = 3; e < 15; e += 2) u = fmax3(u, x[COLS * q + k + e], x[COLS * q + k + e + 1]);
+                                    v = fmax3(v, u, x[COLS * q + k + 15]);
+                                }
+                                mx = fmaxf(mx, fmaf(v, factor(w.x, h * HG + q), w.y));
+                            }
+                            return mx;
+                        };
+                        // P of a half to TMEM, its sums to l and the weights (their order: see the caller)
+                        auto exponentials = [&](int h, const float (&x)[HALF]) {
+                            uint32_t pk[HALF / 2];
+                            float add_l = 0.f;
+                            float* dst = gsum + static_cast<long long>(h) * (per_tile / 2) * a.rows;
+#pragma unroll
+                            for (int q = 0; q < HG; ++q) {
+                                const float4 w = sm.sc[sc][h * HG + q];
+                                const float f = factor(w.x, h * HG + q), add = nm + w.y;
+                                const float sum = exp_pairs<COLS>(x + COLS * q, f2_pack(f, f), f2_pack(add, add), pk + COLS / 2 * q) * w.z;
+                                add_l += sum;
+                                if (MASS) {
+                                    // log2 of the sums of each 64 keys, or of a smaller block
+                                    weight += sum;
+                                    if (G == 2 || ((q + 1) & (per_sum - 1)) == 0) {
+                                        const int k = h * (per_tile / 2) + q / per_sum;
+                                        if (live && k < gsum_left) *dst = __log2f(weight) - nm;
+                                        dst += a.rows;
+                                        weight = 0.f;
+                                    }
+                                }
+                            }
+                            l += add_l;
+                            tmem_store(tm_p + h * (HALF / 2), pk);
+                        };
+                        float x[HALF];
+                        load(0, x);
+                        float mx = maximum(0, x);
+                        load(1, x);
+                        mx = fmaxf(mx, maximum(1, x));
+                        if (const uint32_t bad = sm.sc_nan[sc]; bad)
+                            nan_value |= (bad & ((1u << ((seen + COLS - 1) / COLS)) - 1u)) != 0;
+                        raise = mx > m + RAISE || (m == -INFINITY && mx > m);
+                        if (raise) {
+                            alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+                            m = mx;
+                            l *= alpha;
                         }
-                    }
-                    l += add_l;
+                        nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
+                        // P is free once P V of the step before is done; O then holds every earlier step
+                        if (!mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc)) return false;
+                        tc_fence_after();
+                        exponentials(1, x);
+                        load(0, x);
+                        tc_fence_before();
+                        mbar_arrive(smem_addr(&sm.s_free[s]));
+                        exponentials(0, x);
+                        return true;
+                    };
+                    if (!(ok = __any_sync(0xffffffffu, seen < BN) ? step(std::true_type{}) : step(std::false_type{}))) break;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
-                    // P is free once P V of the step before is done; O then holds every earlier step
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
-                    tc_fence_after();
                     if (__any_sync(0xffffffffu, raise && j > j0)) {
                         const float al = raise && j > j0 ? alpha : 1.f;
-#pragma unroll 1
-                        for (int i = 0; i < HD / 32; ++i) {
-                            uint32_t ro[32];
-                            tmem_ld32(tm_o + i * 32, ro);
-                            tmem_wait_ld_dep(ro);
+                        uint32_t ro[HD];
+                        tmem_load(tm_o, ro);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * al);
-                            tmem_st32(tm_o + i * 32, ro);
-                            tmem_wait_st();
-                        }
+                        for (int e = 0; e < HD; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * al);
+                        tmem_store(tm_o, ro);
                     }
-#pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) tmem_st16(tm_p + i * 16, pk + i * 16);
-                    tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(smem_addr(&sm.p_full[s]));
-                    if (!PAIR && MASS) {                         // the other slot's tile
-                        gsum += static_cast<long long>(per_tile) * a.rows;
-                        gsum_left -= per_tile;
+                    if (MASS) {                                      // past this tile, and the other slot's
+                        gsum += static_cast<long long>(per_tile) * STEP * a.rows;
+                        gsum_left -= per_tile * STEP;
                     }
                 }
                 if (!ok) break;
@@ -631,10 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             float o[HD];
             if (j0 < n) {
                 uint32_t ro[HD];
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i) tmem_ld32(tm_o + i * 32, sub32(ro, i * 32));
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i) tmem_wait_ld_dep(sub32(ro, i * 32));
+                tmem_load(tm_o, ro);
 #pragma unroll
                 for (int e = 0; e < HD; ++e) o[e] = __uint_as_float(ro[e]);
                 tc_fence_before();
