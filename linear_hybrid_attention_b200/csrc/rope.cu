@@ -12,15 +12,15 @@
 // Angles.  The frequency of pair i is held as turns a position in 64-bit fixed
 // point, T_i = f_i / 2 pi * 2^64; the low 64 bits of pos * T_i are then the
 // fraction of a turn, exact for any 32-bit position up to the rounding of T_i
-// (2^-65 turns a position).  Its top 32 bits go to sincospi, so a far position
+// (2^-65 turns a position).  Its top 32 bits go to sin and cos, so a far position
 // costs no more and loses nothing against a near one.
 //
 // Both directions are HBM streams (a row in, a row out; backward two in, one
 // out).  Four lanes hold a row, 16 features each, chosen so that both halves of
 // every rotated pair lie in one thread: no exchange but two shuffles for the
 // row's sums, and one kernel for both pair layouts.  A thread keeps the sines
-// of its 8 pairs and runs over HEADS heads of its token with the loads of
-// UNROLL rows in flight.
+// of its 8 pairs and runs over the heads of its token, the loads of the next rows
+// in flight while it works on these.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -34,7 +34,6 @@ constexpr int HD = 64;
 constexpr int THREADS = 256;
 constexpr int TOK = THREADS / 4;   // tokens a CTA works on at a time
 constexpr int MAX_CTAS = 4096;     // of a backward launch (its partial sums)
-constexpr long long MAX_GX = 1 << 24;  // of a forward launch (a CTA then takes several groups of tokens)
 
 struct View {
     long long b, h, t;             // strides in elements
@@ -47,7 +46,7 @@ struct Side {
     View xs, gs, os;
     const float *w, *bias;         // [64] or NULL
     float *dw, *db;                // [64] or NULL (backward)
-    int heads, slices;             // heads, and CTAs along y that share them
+    int heads, ctas;               // heads, and the CTAs that share the tensor's items
 };
 
 struct Args {
@@ -62,82 +61,130 @@ struct Args {
     float* partial;                // backward: [CTA][2][64]
 };
 
-ZB_DEVINL void unpack8(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+typedef uint64_t f2;               // two fp32 in a register pair
+ZB_DEVINL float total(f2 v) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return x + y;
+}
+
+// A thread's 16 features of a row, two by two: v[0..3] the first members of its
+// eight rotated pairs, v[4..7] the second ones.  In the half layout those are its
+// two chunks of 8, interleaved the even and the odd features of both.
+template <bool HALF>
+ZB_DEVINL void unpack(const uint4& x, const uint4& y, f2* v) {
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
+        if (HALF) {
+            v[i] = f2_pack(bf16_lo(w[i]), bf16_hi(w[i]));
+            v[4 + i] = f2_pack(bf16_lo(w[4 + i]), bf16_hi(w[4 + i]));
+        } else {
+            v[i] = f2_pack(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+            v[4 + i] = f2_pack(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+        }
     }
 }
-ZB_DEVINL uint4 pack8(const float* f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+template <bool HALF>
+ZB_DEVINL void pack(const f2* v, uint4& x, uint4& y) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float p0, p1, q0, q1;
+        f2_unpack(v[i], p0, p1);
+        f2_unpack(v[4 + i], q0, q1);
+        if (HALF) {
+            w[i] = pack_bf16x2(p0, p1);
+            w[4 + i] = pack_bf16x2(q0, q1);
+        } else {
+            w[2 * i] = pack_bf16x2(p0, q0);
+            w[2 * i + 1] = pack_bf16x2(p1, q1);
+        }
+    }
+    x = make_uint4(w[0], w[1], w[2], w[3]);
+    y = make_uint4(w[4], w[5], w[6], w[7]);
 }
+// The feature that element i of those 16 is.
+template <bool HALF>
+ZB_DEVINL int feature(int i, int c0, int c1) {
+    if (HALF) return i < 8 ? c0 * 8 + i : c1 * 8 + i - 8;
+    const int j = i & 7;
+    return (j < 4 ? c0 * 8 + 2 * j : c1 * 8 + 2 * (j - 4)) + (i >> 3);
+}
+
 ZB_DEVINL float row_sum(float v) {   // over the row's four lanes
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// Rotate the thread's 16 features by its 8 angles: pairs (f[j], f[8 + j]) in the
-// half layout, (f[2j], f[2j + 1]) interleaved.
-ZB_DEVINL void rotate(float* f, const float* c, const float* s, bool half, bool back) {
-    if (half) {
+// (x, y) by the angle of (c, s): x c - y s, y c + x s, with -s given beside s.
+ZB_DEVINL void rotate(f2* v, const f2* c, const f2* s, const f2* ns) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float sj = back ? -s[j] : s[j];
-            const float a = f[j], b = f[8 + j];
-            f[j] = a * c[j] - b * sj;
-            f[8 + j] = b * c[j] + a * sj;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float sj = back ? -s[j] : s[j];
-            const float a = f[2 * j], b = f[2 * j + 1];
-            f[2 * j] = a * c[j] - b * sj;
-            f[2 * j + 1] = b * c[j] + a * sj;
-        }
+    for (int i = 0; i < 4; ++i) {
+        const f2 x = v[i], y = v[4 + i];
+        v[i] = f2_fma(x, c[i], f2_mul(y, ns[i]));
+        v[4 + i] = f2_fma(y, c[i], f2_mul(x, s[i]));
     }
 }
 
-// Normalise in place; returns r.
+// v <- the row, centred where the norm is a layer norm; returns 1 / its deviation.  The
+// variance is taken of the centred row: a second pass over registers, no cancellation.
 template <int KIND>
-ZB_DEVINL float normalise(float* f, float eps) {
+ZB_DEVINL float centre(f2* v, float eps) {
     if (KIND == ZB_NORM_NONE) return 1.f;
     if (KIND == ZB_NORM_LAYER) {
-        float m = 0.f;
+        const float m = row_sum(total(f2_add(f2_add(f2_add(v[0], v[1]), f2_add(v[2], v[3])),
+                                             f2_add(f2_add(v[4], v[5]), f2_add(v[6], v[7]))))) * (-1.f / HD);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m += f[i];
-        m = row_sum(m) * (1.f / HD);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] -= m;
+        for (int i = 0; i < 8; ++i) v[i] = f2_add(v[i], f2_pack(m, m));
     }
-    float q = 0.f;
+    f2 q0 = f2_mul(v[0], v[0]), q1 = f2_mul(v[1], v[1]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q += f[i] * f[i];
-    const float r = rsqrtf(row_sum(q) * (1.f / HD) + eps);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= r;
-    return r;
+    for (int i = 2; i < 8; i += 2) {
+        q0 = f2_fma(v[i], v[i], q0);
+        q1 = f2_fma(v[i + 1], v[i + 1], q1);
+    }
+    return rsqrtf(row_sum(total(f2_add(q0, q1))) * (1.f / HD) + eps);
 }
 
-template <int KIND, bool BACK, int UNROLL>
-__global__ void __launch_bounds__(THREADS, 2) row_kernel(const Args a) {
-    // y index -> tensor and its slice of heads
-    const bool second = static_cast<int>(blockIdx.y) >= a.side[0].slices;
+// sin and cos of a fraction of a turn (turns * 2^32).  After the exact reduction
+// the hardware's approximation is within 2^-20 of either, eleven bits below the
+// bf16 result; sincospi costs 8 pairs some 400 instructions against 100.
+ZB_DEVINL void sincos_turns(int frac, float& sn, float& cs) {
+    const float x = static_cast<float>(frac) * (3.14159265358979f * 0x1p-31f);
+    asm("sin.approx.ftz.f32 %0, %1;" : "=f"(sn) : "f"(x));
+    asm("cos.approx.ftz.f32 %0, %1;" : "=f"(cs) : "f"(x));
+}
+
+// rows of a thread under way, rows it works on together, CTAs an SM
+template <int KIND, bool BACK>
+struct Plan {
+    static constexpr int ROWS = BACK ? 1 : 2;
+    static constexpr int CTAS = BACK ? 2 : KIND == ZB_NORM_NONE ? 3 : 2;
+};
+
+template <int KIND, bool BACK, bool HALF>
+__global__ void __launch_bounds__(THREADS, Plan<KIND, BACK>::CTAS) row_kernel(const Args a) {
+    constexpr int ROWS = Plan<KIND, BACK>::ROWS;
+    constexpr bool NORM = KIND != ZB_NORM_NONE;
+
+    // the CTA's tensor and its part of that tensor's (group of TOK tokens, head) items
+    const bool second = static_cast<int>(blockIdx.x) >= a.side[0].ctas;
     const Side& sd = second ? a.side[1] : a.side[0];
-    const int slice = second ? blockIdx.y - a.side[0].slices : blockIdx.y;
-    const int h0 = static_cast<int>(static_cast<long long>(sd.heads) * slice / sd.slices);
-    const int h1 = static_cast<int>(static_cast<long long>(sd.heads) * (slice + 1) / sd.slices);
+    const int cta = second ? blockIdx.x - a.side[0].ctas : blockIdx.x;
+    const int heads = sd.heads;
+    const long long items = (a.tokens + TOK - 1) / TOK * heads;
+    const long long each = items / sd.ctas, more = items - each * sd.ctas;   // the first `more` take one more
+    const long long i0 = each * cta + (cta < more ? cta : more);
+    long long left = each + (cta < more), group = i0 / heads;
+    int h0 = static_cast<int>(i0 - group * heads);
 
     const int p = threadIdx.x & 3;
-    const bool half = a.half != 0;
     const bool turned = p < a.rot / 16;
     const int pairs = a.rot / (2 * a.axes);          // of an axis
     int c0 = 2 * p, c1 = 2 * p + 1, axis = 0, pair0 = 0;
     if (turned) {
-        if (half) {                                  // chunk c0 of an axis' part and its partner
+        if (HALF) {                                  // chunk c0 of an axis' part and its partner
             const int hc = pairs / 8;
             axis = p / hc;
             const int i = p - axis * hc;
@@ -149,130 +196,196 @@ __global__ void __launch_bounds__(THREADS, 2) row_kernel(const Args a) {
             pair0 = p * 8 - axis * pairs;
         }
     }
-    float w[16], bias[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int e = (i < 8 ? c0 * 8 : c1 * 8 - 8) + i;
-        w[i] = (KIND != ZB_NORM_NONE && sd.w) ? __ldg(sd.w + e) : 1.f;
-        if (!BACK) bias[i] = (KIND == ZB_NORM_LAYER && sd.bias) ? __ldg(sd.bias + e) : 0.f;
+    // weights and biases in the order of the threads' elements
+    __shared__ ulonglong2 weights[4][4], biases[4][4];
+    if (NORM) {
+        if (threadIdx.x < 4 * 16) {
+            const int l = threadIdx.x & 3, i = threadIdx.x >> 2;
+            const int e = feature<HALF>(i, c0, c1);  // l == p
+            reinterpret_cast<float*>(weights[l])[i] = sd.w ? __ldg(sd.w + e) : 1.f;
+            if (KIND == ZB_NORM_LAYER && !BACK) reinterpret_cast<float*>(biases[l])[i] = sd.bias ? __ldg(sd.bias + e) : 0.f;
+        }
+        __syncthreads();
     }
-    float dw[16], db[16];
+    auto weight = [&](int i) { return i & 1 ? weights[p][i >> 1].y : weights[p][i >> 1].x; };
+    auto bias = [&](int i) { return i & 1 ? biases[p][i >> 1].y : biases[p][i >> 1].x; };
+    f2 dw[8], db[8];
     if (BACK) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dw[i] = db[i] = 0.f;
+        for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0ull;
     }
 
-    const long long step = static_cast<long long>(gridDim.x) * TOK;
-    for (long long base = static_cast<long long>(blockIdx.x) * TOK; base < a.tokens; base += step) {
-        const long long u = base + (threadIdx.x >> 2);
+    const long long xh = sd.xs.h / 8, gh = sd.gs.h / 8, oh = sd.os.h / 8;
+#pragma unroll 1
+    while (left > 0) {
+        const int n = heads - h0 < left ? heads - h0 : static_cast<int>(left);   // rows of this group
+        const long long u = group * TOK + (threadIdx.x >> 2);
         const bool live = u < a.tokens;              // dead lanes still join the shuffles
-        const long long b = live ? u / a.n : 0, t = live ? u - b * a.n : 0;
-        float cs[8], sn[8];
-        if (turned && live) {
-            const int pos = __ldg(a.pos + b * a.pos_b + axis * a.n + t);
+        long long b = 0, t = live ? u : 0;
+        if (a.tokens != a.n) {
+            b = (a.tokens >> 32) ? t / a.n : static_cast<uint32_t>(t) / static_cast<uint32_t>(a.n);
+            t -= b * a.n;
+        }
+        const uint4* x = reinterpret_cast<const uint4*>(sd.x + b * sd.xs.b + t * sd.xs.t + h0 * sd.xs.h);
+        const uint4* g = BACK ? reinterpret_cast<const uint4*>(sd.g + b * sd.gs.b + t * sd.gs.t + h0 * sd.gs.h) : nullptr;
+        uint4* o = reinterpret_cast<uint4*>(sd.out + b * sd.os.b + t * sd.os.t + h0 * sd.os.h);
+        // the next ROWS rows are on their way while these are worked on
+        uint4 xv[ROWS][2], gv[2];
+        auto load = [&](int r) {
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                if (k == 0 || r + k < n) {           // otherwise an old row again, not stored
+                    xv[k][0] = __ldg(x + c0);
+                    xv[k][1] = __ldg(x + c1);
+                    x += xh;
+                }
+            }
+            if (BACK) {
+                gv[0] = live ? __ldg(g + c0) : make_uint4(0, 0, 0, 0);
+                gv[1] = live ? __ldg(g + c1) : make_uint4(0, 0, 0, 0);
+                g += gh;
+            }
+        };
+#pragma unroll
+        for (int k = 1; k < ROWS; ++k) xv[k][0] = xv[k][1] = make_uint4(0, 0, 0, 0);
+        load(0);
+        // forward, a row is r (x w c - y w' s) + b: weights and biases turned once a token
+        f2 ca[4], cb[4], sa[4], sb[4], z[8];
+        {
+            float c[8], s[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos)) *
-                                              static_cast<unsigned long long>(__ldg(a.turns + pair0 + j));
-                sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn[j], &cs[j]);
-                sn[j] *= a.mag;
-                cs[j] *= a.mag;
+                c[j] = 1.f;
+                s[j] = 0.f;
             }
-        }
-        const uint16_t* x = sd.x + b * sd.xs.b + t * sd.xs.t;
-        const uint16_t* g = BACK ? sd.g + b * sd.gs.b + t * sd.gs.t : nullptr;
-        uint16_t* o = sd.out + b * sd.os.b + t * sd.os.t;
-        for (int h = h0; h < h1; h += UNROLL) {
-            uint4 xv[UNROLL][2], gv[UNROLL][2];
+            if (turned) {
+                const unsigned long long pos = static_cast<long long>(__ldg(a.pos + b * a.pos_b + axis * a.n + t));
+                const float way = BACK || a.inverse ? -a.mag : a.mag;
 #pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                const bool on = live && h + k < h1;
-                const uint4* r = reinterpret_cast<const uint4*>(x + (h + k) * sd.xs.h);
-                xv[k][0] = on ? __ldg(r + c0) : make_uint4(0, 0, 0, 0);
-                xv[k][1] = on ? __ldg(r + c1) : make_uint4(0, 0, 0, 0);
-                if (BACK) {
-                    const uint4* q = reinterpret_cast<const uint4*>(g + (h + k) * sd.gs.h);
-                    gv[k][0] = on ? __ldg(q + c0) : make_uint4(0, 0, 0, 0);
-                    gv[k][1] = on ? __ldg(q + c1) : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 8; ++j) {
+                    const unsigned long long ph = pos * static_cast<unsigned long long>(__ldg(a.turns + pair0 + j));
+                    sincos_turns(static_cast<int>(ph >> 32), s[j], c[j]);
+                    c[j] *= a.mag;
+                    s[j] *= way;
                 }
             }
 #pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                float f[16], e[16];
-                unpack8(xv[k][0], f);
-                unpack8(xv[k][1], f + 8);
-                const bool on = live && h + k < h1;
-                // a row that is not there is zeros: with 1 for eps it stays zeros and adds
-                // nothing to the sums
-                const float r = normalise<KIND>(f, on ? a.eps : 1.f);
+            for (int i = 0; i < 4; ++i) {
+                ca[i] = cb[i] = f2_pack(c[2 * i], c[2 * i + 1]);
+                sa[i] = f2_pack(s[2 * i], s[2 * i + 1]);
+                sb[i] = f2_pack(-s[2 * i], -s[2 * i + 1]);
+                if (!BACK && KIND == ZB_NORM_LAYER) {
+                    z[i] = bias(i);
+                    z[4 + i] = bias(4 + i);
+                }
+            }
+            if (!BACK && KIND == ZB_NORM_LAYER && turned) rotate(z, ca, sa, sb);
+            if (!BACK && NORM) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f2 wa = weight(i), wb = weight(4 + i);
+                    ca[i] = f2_mul(ca[i], wa);
+                    sa[i] = f2_mul(sa[i], wa);
+                    cb[i] = f2_mul(cb[i], wb);
+                    sb[i] = f2_mul(sb[i], wb);
+                }
+            }
+        }
+#pragma unroll 1
+        for (int r = 0; r < n; r += ROWS) {
+            f2 f[ROWS][8], e[8];
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) unpack<HALF>(xv[k][0], xv[k][1], f[k]);
+            if (BACK) unpack<HALF>(gv[0], gv[1], e);
+            if (r + ROWS < n) load(r + ROWS);
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                const float inv = centre<KIND>(f[k], a.eps);
+                const f2 inv2 = f2_pack(inv, inv);
                 if (BACK) {
-                    unpack8(gv[k][0], e);
-                    unpack8(gv[k][1], e + 8);
-                    if (turned) rotate(e, cs, sn, half, true);
-                    float m1 = 0.f, m0 = 0.f;
+                    if (turned) rotate(e, ca, sa, sb);
+                    f2 t1 = 0ull, t0 = 0ull;
+                    if (NORM) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (KIND != ZB_NORM_NONE) dw[i] += e[i] * f[i];
-                        if (KIND == ZB_NORM_LAYER) db[i] += e[i];
-                        e[i] *= w[i];
-                        m1 += e[i] * f[i];
-                        m0 += e[i];
+                        for (int i = 0; i < 8; ++i) {
+                            f[k][i] = f2_mul(f[k][i], inv2);
+                            dw[i] = f2_fma(e[i], f[k][i], dw[i]);
+                            if (KIND == ZB_NORM_LAYER) db[i] = f2_add(db[i], e[i]);
+                            e[i] = f2_mul(e[i], weight(i));
+                            t1 = f2_fma(e[i], f[k][i], t1);
+                            if (KIND == ZB_NORM_LAYER) t0 = f2_add(t0, e[i]);
+                        }
+                        const float m1 = row_sum(total(t1)) * (-1.f / HD);
+                        const float m0 = KIND == ZB_NORM_LAYER ? row_sum(total(t0)) * (-1.f / HD) : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (KIND == ZB_NORM_LAYER) e[i] = f2_add(e[i], f2_pack(m0, m0));
+                            e[i] = f2_mul(inv2, f2_fma(f[k][i], f2_pack(m1, m1), e[i]));
+                        }
                     }
-                    m1 = KIND != ZB_NORM_NONE ? row_sum(m1) * (1.f / HD) : 0.f;
-                    m0 = KIND == ZB_NORM_LAYER ? row_sum(m0) * (1.f / HD) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = r * (e[i] - m0 - f[i] * m1);
+                    if (live) pack<HALF>(e, o[c0], o[c1]);
                 } else {
-                    if (KIND != ZB_NORM_NONE) {
+                    f2* v = f[k];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = KIND == ZB_NORM_LAYER ? f[i] * w[i] + bias[i] : f[i] * w[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const f2 xa = v[i], xb = v[4 + i];
+                        if (turned) {
+                            v[i] = f2_fma(xa, ca[i], f2_mul(xb, sb[i]));
+                            v[4 + i] = f2_fma(xb, cb[i], f2_mul(xa, sa[i]));
+                        } else if (NORM) {
+                            v[i] = f2_mul(xa, ca[i]);
+                            v[4 + i] = f2_mul(xb, cb[i]);
+                        }
                     }
-                    if (turned) rotate(f, cs, sn, half, a.inverse != 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (KIND == ZB_NORM_LAYER) v[i] = f2_fma(v[i], inv2, z[i]);
+                        if (KIND == ZB_NORM_RMS) v[i] = f2_mul(v[i], inv2);
+                    }
+                    if (live && (k == 0 || r + k < n)) pack<HALF>(v, o[c0], o[c1]);
                 }
-                if (on) {
-                    uint4* q = reinterpret_cast<uint4*>(o + (h + k) * sd.os.h);
-                    q[c0] = pack8(f);
-                    q[c1] = pack8(f + 8);
-                }
+                o += oh;
             }
         }
+        left -= n;
+        h0 = 0;
+        ++group;
     }
     if (BACK && KIND != ZB_NORM_NONE) {
         // the CTA's sums: rows of a warp by shuffles, warps through shared memory in order
         __shared__ float red[THREADS / 32][2][HD];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
+            float v[4];
+            f2_unpack(dw[i], v[0], v[1]);
+            f2_unpack(db[i], v[2], v[3]);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-                db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int l = 4; l < 32; l <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], l);
             }
-        }
-        if (lane_id() < 4) {
+            if (lane_id() < 4) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = (i < 8 ? c0 * 8 : c1 * 8 - 8) + i;
-                red[warp_id()][0][e] = dw[i];
-                red[warp_id()][1][e] = db[i];
+                for (int k = 0; k < 4; ++k) red[warp_id()][k >> 1][feature<HALF>(2 * i + (k & 1), c0, c1)] = v[k];
             }
         }
         __syncthreads();
         if (threadIdx.x < 2 * HD) {
-            float s = 0.f;
-            for (int k = 0; k < THREADS / 32; ++k) s += (&red[k][0][0])[threadIdx.x];
-            a.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * HD + threadIdx.x] = s;
+            float v = 0.f;
+            for (int k = 0; k < THREADS / 32; ++k) v += (&red[k][0][0])[threadIdx.x];
+            a.partial[static_cast<long long>(blockIdx.x) * 2 * HD + threadIdx.x] = v;
         }
     }
 }
 
 // dw and db of one tensor from the CTAs' partial sums, in a fixed order, fp64.
 // Grid: 8 blocks of 8 features x 2 (dw, db) x 2 (queries, keys).
-__global__ void __launch_bounds__(256) reduce_kernel(const float* partial, int gx, Args a) {
+__global__ void __launch_bounds__(256) reduce_kernel(const float* partial, Args a) {
     const int which = blockIdx.y & 1, tensor = blockIdx.y >> 1;
     float* out = which ? a.side[tensor].db : a.side[tensor].dw;
     if (!out) return;
-    const int first = tensor ? a.side[0].slices * gx : 0;
-    const int count = a.side[tensor].slices * gx;
+    const int first = tensor ? a.side[0].ctas : 0;
+    const int count = a.side[tensor].ctas;
     const int f = threadIdx.x & 7, part = threadIdx.x >> 3;   // 32 parts
     double s = 0.0;
     for (int c = part; c < count; c += 32)
@@ -346,30 +459,39 @@ void put_rotation(Args& a, const zb_rotation& r) {
     a.inverse = r.inverse;
 }
 
-// Heads are shared out over y so that the launch has about eight CTAs an SM
-// where the tokens alone do not give them; every slice pays for the sines of
-// its tokens again.
-void slice_heads(Args& a, long long gx, int sms) {
-    const int total = a.side[0].heads + a.side[1].heads;
-    long long want = (8ll * sms + gx - 1) / gx;
-    if (want > total) want = total;
+// The CTAs that fit on the device at once, shared out between the tensors by
+// their items (a group of TOK tokens of one head) and within a tensor evenly:
+// no last wave that leaves SMs idle.
+void share_ctas(Args& a, int resident) {
+    const long long groups = (a.tokens + TOK - 1) / TOK;
+    const long long total = groups * (static_cast<long long>(a.side[0].heads) + a.side[1].heads);
     for (int s = 0; s < 2; ++s) {
-        const int h = a.side[s].heads;
-        long long k = (want * h + total - 1) / total;
-        if (k > h) k = h;
-        if (k > 16000) k = 16000;
-        a.side[s].slices = h ? static_cast<int>(k < 1 ? 1 : k) : 0;
+        const long long items = groups * a.side[s].heads;
+        long long k = total <= resident ? items : static_cast<long long>(static_cast<double>(items) / total * resident + 0.5);
+        if (k > items) k = items;
+        a.side[s].ctas = items ? static_cast<int>(k < 1 ? 1 : k) : 0;
     }
 }
 
-template <bool BACK, int UNROLL>
-zb_status launch(const Args& a, int kind, dim3 grid, cudaStream_t st) {
-    switch (kind) {
-        case ZB_NORM_RMS: row_kernel<ZB_NORM_RMS, BACK, UNROLL><<<grid, THREADS, 0, st>>>(a); break;
-        case ZB_NORM_LAYER: row_kernel<ZB_NORM_LAYER, BACK, UNROLL><<<grid, THREADS, 0, st>>>(a); break;
-        default: row_kernel<ZB_NORM_NONE, BACK, UNROLL><<<grid, THREADS, 0, st>>>(a); break;
-    }
+template <int KIND, bool BACK, bool HALF>
+zb_status launch_layout(Args& a, const DeviceInfo& dev, cudaStream_t st) {
+    share_ctas(a, Plan<KIND, BACK>::CTAS * dev.sm_count);
+    row_kernel<KIND, BACK, HALF><<<a.side[0].ctas + a.side[1].ctas, THREADS, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}
+
+template <int KIND, bool BACK>
+zb_status launch_kind(Args& a, const DeviceInfo& dev, cudaStream_t st) {
+    return a.half ? launch_layout<KIND, BACK, true>(a, dev, st) : launch_layout<KIND, BACK, false>(a, dev, st);
+}
+
+template <bool BACK>
+zb_status launch(Args& a, int kind, const DeviceInfo& dev, cudaStream_t st) {
+    switch (kind) {
+        case ZB_NORM_RMS: return launch_kind<ZB_NORM_RMS, BACK>(a, dev, st);
+        case ZB_NORM_LAYER: return launch_kind<ZB_NORM_LAYER, BACK>(a, dev, st);
+        default: return launch_kind<ZB_NORM_NONE, BACK>(a, dev, st);
+    }
 }
 
 }  // namespace rope
@@ -422,11 +544,7 @@ extern "C" zb_status zb_rope(const uint16_t* X, zb_rows x_rows, int32_t batch, i
     a.tokens = static_cast<long long>(batch) * n_tokens;
     a.n = n_tokens;
     rope::put_rotation(a, rot);
-    long long gx = (a.tokens + rope::TOK - 1) / rope::TOK;
-    if (gx > rope::MAX_GX) gx = rope::MAX_GX;
-    rope::slice_heads(a, gx, dev.sm_count);
-    return rope::launch<false, 4>(a, ZB_NORM_NONE, dim3(static_cast<unsigned>(gx), a.side[0].slices),
-                                  static_cast<cudaStream_t>(stream));
+    return rope::launch<false>(a, ZB_NORM_NONE, dev, static_cast<cudaStream_t>(stream));
 }
 
 namespace {
@@ -463,12 +581,7 @@ extern "C" zb_status zb_qk_norm_rope(const uint16_t* Q, zb_rows q_rows, int32_t 
     a.n = n_tokens;
     a.eps = norm.eps;
     rope::put_rotation(a, rot);
-    long long gx = (a.tokens + rope::TOK - 1) / rope::TOK;
-    if (gx > rope::MAX_GX) gx = rope::MAX_GX;
-    rope::slice_heads(a, gx, dev.sm_count);
-    return rope::launch<false, 4>(a, norm.kind,
-                                  dim3(static_cast<unsigned>(gx), a.side[0].slices + a.side[1].slices),
-                                  static_cast<cudaStream_t>(stream));
+    return rope::launch<false>(a, norm.kind, dev, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t zb_qk_norm_rope_backward_workspace_bytes(void) {
@@ -513,22 +626,11 @@ extern "C" zb_status zb_qk_norm_rope_backward(const uint16_t* dQo, const uint16_
     a.eps = norm.eps;
     rope::put_rotation(a, rot);
     a.partial = static_cast<float*>(ws);
-    long long gx = (a.tokens + rope::TOK - 1) / rope::TOK;
-    if (gx > 2ll * dev.sm_count) gx = 2ll * dev.sm_count;   // the CTAs that fit at once: few partial sums
-    rope::slice_heads(a, gx, dev.sm_count);
-    while (gx * (a.side[0].slices + a.side[1].slices) > rope::MAX_CTAS) {
-        if (a.side[0].slices > 1 || a.side[1].slices > 1) {
-            a.side[0].slices = (a.side[0].slices + 1) / 2;
-            a.side[1].slices = (a.side[1].slices + 1) / 2;
-        } else {
-            gx = rope::MAX_CTAS / 2;
-        }
-    }
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = rope::launch<true, 2>(a, norm.kind, dim3(static_cast<unsigned>(gx), a.side[0].slices + a.side[1].slices), st);
+    e = rope::launch<true>(a, norm.kind, dev, st);
     if (e != ZB_OK) return e;
     if (a.side[0].dw || a.side[0].db || a.side[1].dw || a.side[1].db) {
-        rope::reduce_kernel<<<dim3(8, 4), 256, 0, st>>>(a.partial, static_cast<int>(gx), a);
+        rope::reduce_kernel<<<dim3(8, 4), 256, 0, st>>>(a.partial, a);
         if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
     }
     return ZB_OK;
