@@ -16,11 +16,24 @@
 // costs no more and loses nothing against a near one.
 //
 // Both directions are HBM streams (a row in, a row out; backward two in, one
-// out).  Four lanes hold a row, 16 features each, chosen so that both halves of
-// every rotated pair lie in one thread: no exchange but two shuffles for the
-// row's sums, and one kernel for both pair layouts.  A thread keeps the sines
-// of its 8 pairs and runs over the heads of its token, the loads of the next rows
-// in flight while it works on these.
+// out) that only reach the memory's rate if their arithmetic stays small: a row
+// has 64 features and some 95 instructions a thread here.  Four lanes hold a
+// row, 16 features each, chosen so that both halves of every rotated pair lie in
+// one thread: no exchange but two shuffles for each of the row's sums, and one
+// kernel for both pair layouts.  Features are worked on as packed pairs, and
+// forward the weights and biases are turned once a token together with the sines,
+// so that a row costs one rotation whatever its norm.  A thread runs over the
+// heads of its token with the next rows' loads under way; the items are shared
+// out evenly over the CTAs that fit at once.
+//
+// Measured (B200): rotation alone, 16 heads of 43,968 tokens, 32 us (27 at the
+// copy rate); layer norm and rotation of 16 + 16 heads of 43,968 tokens 67 us
+// (54); rms norm of 16 + 4 heads of 2 x 10,992 tokens 24 us forward, 40 + 3
+// backward (17 and 25).  Before: scalar arithmetic, weights in registers and
+// sincospi 37, 83, 32 and 48 + 6 us; rows copied ahead through shared memory
+// instead of registers 38, 98, 35 and 57 (the shared memory's own bandwidth);
+// three CTAs an SM instead of two 38 (spills); groups of tokens of four heads
+// side by side 38.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -156,16 +169,11 @@ ZB_DEVINL void sincos_turns(int frac, float& sn, float& cs) {
     asm("cos.approx.ftz.f32 %0, %1;" : "=f"(cs) : "f"(x));
 }
 
-// rows of a thread under way, rows it works on together, CTAs an SM
-template <int KIND, bool BACK>
-struct Plan {
-    static constexpr int ROWS = BACK ? 1 : 2;
-    static constexpr int CTAS = BACK ? 2 : KIND == ZB_NORM_NONE ? 3 : 2;
-};
+constexpr int CTAS = 2;                // an SM: 128 registers a thread; with 80 (three) most kernels spill
 
 template <int KIND, bool BACK, bool HALF>
-__global__ void __launch_bounds__(THREADS, Plan<KIND, BACK>::CTAS) row_kernel(const Args a) {
-    constexpr int ROWS = Plan<KIND, BACK>::ROWS;
+__global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
+    constexpr int ROWS = BACK ? 1 : 2;               // worked on together
     constexpr bool NORM = KIND != ZB_NORM_NONE;
 
     // the CTA's tensor and its part of that tensor's (group of TOK tokens, head) items
@@ -475,7 +483,7 @@ void share_ctas(Args& a, int resident) {
 
 template <int KIND, bool BACK, bool HALF>
 zb_status launch_layout(Args& a, const DeviceInfo& dev, cudaStream_t st) {
-    share_ctas(a, Plan<KIND, BACK>::CTAS * dev.sm_count);
+    share_ctas(a, CTAS * dev.sm_count);
     row_kernel<KIND, BACK, HALF><<<a.side[0].ctas + a.side[1].ctas, THREADS, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
 }
