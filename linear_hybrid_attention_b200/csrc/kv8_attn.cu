@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     const int h = blockIdx.x, part = blockIdx.y;
     const long long cap = static_cast<long long>(c.slots) * c.block;
     const long long len = head_len(a.lens, h, cap);
-    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
+    const int blocks = static_cast<int>((len + c.block - 1) >> (31 - __clz(c.block)));
     const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
     const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
     const int first = part * 256 + threadIdx.x;      // this thread's first block
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     const zb_kv8& c = a.c;
     const int h = blockIdx.x;
     const long long len = head_len(a.lens, h, static_cast<long long>(c.slots) * c.block);
-    const int blocks = static_cast<int>((len + c.block - 1) / c.block);
+    const int blocks = static_cast<int>((len + c.block - 1) >> (31 - __clz(c.block)));
     const int per_block = c.block > CHUNK ? c.block / CHUNK : 1;
     const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
     const int size = min(c.block, CHUNK);

@@ -132,7 +132,7 @@ template <int FMT>
 __global__ void __launch_bounds__(A_THREADS, 4) append_kernel(const AppendArgs a) {
     const int h = blockIdx.y, unit = blockIdx.x;
     const zb_kv8& c = a.c;
-    const int B = c.block;
+    const int B = c.block, shift = 31 - __clz(B);   // B is a power of two
     const long long cap = static_cast<long long>(c.slots) * B;
     const long long len = __ldg(a.lens + h);
     if (len < 0 || len + a.n > cap) {          // does not fit: the head stays as it is
@@ -142,13 +142,13 @@ __global__ void __launch_bounds__(A_THREADS, 4) append_kernel(const AppendArgs a
         }
         return;
     }
-    const int held = static_cast<int>(len % B);
-    const long long first = len / B;           // logical block that row 0 belongs to
+    const int held = static_cast<int>(len) & (B - 1);
+    const long long first = len >> shift;           // logical block that row 0 belongs to
     const long long rows = held + static_cast<long long>(a.n);
     const int warp = warp_id(), lane = lane_id();
-    const long long blocks = (rows + B - 1) / B;
+    const long long blocks = (rows + B - 1) >> shift;
     const long long row0 = static_cast<long long>(unit) * UNIT + warp * 16;
-    const long long blk = row0 / B;            // of this warp
+    const long long blk = row0 >> shift;            // of this warp
     const bool live = blk < blocks;
     uint4* tail[2] = {reinterpret_cast<uint4*>(c.k_tail) + static_cast<long long>(h) * B * 8,
                       reinterpret_cast<uint4*>(c.v_tail) + static_cast<long long>(h) * B * 8};
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(A_THREADS, 4) append_kernel(const AppendArgs a
         // The rows of the block left in progress, once this CTA has read the old
         // ones (no other CTA reads them: they are all in the first unit).
         __syncthreads();
-        const int left = static_cast<int>(rows % B);
+        const int left = static_cast<int>(rows) & (B - 1);
         const long long last = rows - left;
         for (int i = threadIdx.x; i < left * 8; i += A_THREADS) {
             const long long r = last + (i >> 3);
