@@ -201,6 +201,8 @@ def zb_qk_norm_rope_backward(dQo, dKo, Q, K, pos, turns, norm: str = "rms", wq=N
     dwq, dwk, dbq, dbk = (sums[i] if on else None for i, on in
                           enumerate((kind > 0, kind > 0 and hk > 0, kind == 2, kind == 2 and hk > 0)))
     ws = _ws(int(_lib_handle().zb_qk_norm_rope_backward_workspace_bytes()), dev, ws)
+    if ws.device != dev:
+        raise ValueError(f"ws must be on {dev}, is on {ws.device}")
     _call(dev, "zb_qk_norm_rope_backward", dQo.data_ptr(), _ptr(dKo), Q.data_ptr(), qs, hq, _ptr(K), ks, hk, b, n,
           HEAD_DIM, nm, rot, dQ.data_ptr(), _view(dQ, "dQ")[3], _ptr(dK), zero if dK is None else _view(dK, "dK")[3],
           _ptr(dwq), _ptr(dwk), _ptr(dbq), _ptr(dbk), ws.data_ptr(), ws.numel() * ws.element_size())

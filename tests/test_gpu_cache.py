@@ -342,6 +342,68 @@ def test_attention_is_repeatable_and_bad_tables_are_reported():
         sync_ok()
 
 
+def test_many_rows_are_repeatable_in_graphs_and_streams():
+    import linear_hybrid_attention_b200 as zb
+    lens = [3000, 70, 900]
+    c, ora = _filled(zb, lens, 3008, 64, "int8", 710)
+    n = _ints(lens)
+    Q = [_rand((6, 150, 64), 15 + i) for i in range(2)]
+    want = [zb.zb_kv8_attn(q, c, n, causal=True, want_lse=True) for q in Q]
+    streams = [torch.cuda.Stream() for _ in Q]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(zb.zb_kv8_attn(Q[i], c, n, causal=True, want_lse=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
+    # a captured call with weights follows the lengths
+    c.mass.zero_()
+    with torch.cuda.stream(streams[0]):
+        zb.zb_kv8_attn(Q[0], c, n, add_mass=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        out = zb.zb_kv8_attn(Q[0], c, n, add_mass=True)
+    for now in (lens, [1, 0, 900], [2999, 64, 129]):
+        n.copy_(_ints(now))
+        c.mass.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        mass = c.mass.clone()
+        c.mass.zero_()
+        assert torch.equal(out, zb.zb_kv8_attn(Q[0], c, n, add_mass=True)) and torch.equal(mass, c.mass)
+    sync_ok()
+
+
+@pytest.mark.parametrize("n_q", [1, 40])
+def test_offsets_past_32_bits(n_q):
+    # heads of 2^31 bytes of codes and more, their tokens in the last slots
+    import linear_hybrid_attention_b200 as zb
+    block, fmt, H, N = 128, "int8", 2, 700
+    slots = 2 ** 31 // (block * 64) + 40
+    c = zb.KV8Cache.empty(H, slots * block, block, fmt)
+    assert c.slots == slots
+    c.table.copy_(c.table.flip(1))
+    K, V = _rand((H, N, 64), 720), _rand((H, N, 64), 721)
+    lens = zb.zb_kv8_append(c, K, V, _ints([0] * H))
+    ora = [oracle.Cache8(block, fmt) for _ in range(H)]
+    for h in range(H):
+        ora[h].append(host(K[h]), host(V[h]))
+    Ko, Vo = zb.zb_kv8_read(c, lens, N)
+    for h in range(H):
+        np.testing.assert_array_equal(host(Ko[h]), bf16_round_f64(ora[h].values()[0]))
+        np.testing.assert_array_equal(host(Vo[h]), bf16_round_f64(ora[h].values()[1]))
+    _check_attention(zb, c, ora, [N] * H, 1, n_q, True, 16)
+    table, lens, kept = zb.zb_kv8_evict(c.table, c.mass, lens, block, 3, 1, 1)
+    sync_ok()
+    for h in range(H):
+        assert int(lens[h]) == N - 3 * block and kept[h, 0] == 0 and kept[h, 2] == 5
+        assert torch.equal(table[h, 6:], c.table[h, 6:])
+
+
 # ---------------------------------------------------------------- eviction ----
 @pytest.mark.parametrize("slots,block,budget,sinks,recent", [(1, 16, 1, 0, 1), (9, 16, 4, 1, 2), (9, 64, 3, 1, 2),
                                                              (300, 64, 100, 4, 12), (1500, 16, 1499, 0, 1),

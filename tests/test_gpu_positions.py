@@ -1,8 +1,9 @@
 """Rotary positions and the norm of queries and keys on the GPU, against the fp64 oracle.
 
 Tolerances.  Outputs are rounded to bf16 once: half a step, 2^-8 of the value.  Before that everything is
-fp32 on values no larger than the row's largest M times the magnitude: sincospi, two products and a sum, some
-ten roundings of 2^-24 and the row's statistics (a sum of 64 squares, rsqrt): under 2^-18 M in all.  A weight
+fp32 on values no larger than the row's largest M times the magnitude: sines and cosines off by 2^-20.5 at most,
+two of them in a feature (2^-19.5 M), products and a sum, some ten roundings of 2^-24 and the row's statistics (a sum
+of 64 squares, rsqrt): under 2^-18 M in all.  A weight
 gradient is a sum of n products, at most 100 of them one after another in a thread (sizes below), then trees:
 128 * 2^-24 of the sum of the products' sizes, and the products' own error (see there).
 """
@@ -266,3 +267,76 @@ def test_binding_refusals():
             zb.zb_qk_norm_rope(**{**dict(Q=X, K=X, pos=pos, turns=turns), **over})
     with pytest.raises(ValueError):
         zb.zb_qk_norm_rope_backward(X[:, :2], None, X, None, pos, turns)
+    with pytest.raises(ValueError):
+        zb.zb_qk_norm_rope_backward(X, None, X, None, pos, turns, ws=torch.empty(1 << 22, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("axes,layout,rot", [(1, "half", 64), (1, "interleaved", 48), (2, "half", 64), (2, "interleaved", 32)])
+def test_position_zero_changes_nothing(axes, layout, rot):
+    import linear_hybrid_attention_b200 as zb
+    fr, turns = _freq(zb, rot, axes, "none")
+    X = _rand((2, 3, 70, 64), 40)
+    pos = torch.zeros((1, axes, 70), dtype=torch.int32, device="cuda")
+    for inverse in (False, True):
+        assert torch.equal(zb.zb_rope(X, pos, turns, axes=axes, layout=layout, inverse=inverse), X)
+
+
+# more items than the GPU takes at once: a CTA's share begins and ends inside a token's heads, and groups of
+# tokens cross from one sequence to the next
+MANY = [(3, 7, 3, 4001, "rms", 64, 1, "half", "ntk", 100_000), (2, 5, 5, 5003, "layer", 32, 1, "interleaved", "none", 0),
+        (1, 9, 1, 9000, "layer", 64, 2, "half", "none", 30)]
+
+
+@pytest.mark.parametrize("B,Hq,Hk,N,kind,rot,axes,layout,scaling,far", MANY)
+def test_many_items(B, Hq, Hk, N, kind, rot, axes, layout, scaling, far):
+    zb, Q, K, (wq, wk, bq, bk), pos, fr, turns, how, ora = _norm_case(B, Hq, Hk, N, kind, rot, axes, layout, scaling,
+                                                                      far, 51)
+    dev = lambda t: None if t is None else t.cuda()
+    n64 = lambda t: None if t is None else t.double().numpy()
+    eps = float(np.float32(1e-6))
+    pos_d = pos.cuda()
+    y = zb.zb_rope(Q, pos_d, turns, axes=axes, layout=layout, magnitude=fr.magnitude)
+    _close(y, oracle.rope(host(Q), pos.numpy(), fr.radians.numpy(), **ora),
+           np.abs(host(Q)).max(-1, keepdims=True) * fr.magnitude)
+    outs = zb.zb_qk_norm_rope(Q, K, pos_d, turns, bq=dev(bq), bk=dev(bk), **how)
+    gq, gk = _rand((B, Hq, N, 64), 52), _rand((B, Hk, N, 64), 53)
+    grad = zb.zb_qk_norm_rope_backward(gq, gk, Q, K, pos_d, turns, **how)
+    sync_ok()
+    for got, x, w, b, g, dx, dw, db in ((outs[0], Q, wq, bq, gq, grad[0], grad[2], grad[4]),
+                                        (outs[1], K, wk, bk, gk, grad[1], grad[3], grad[5])):
+        plain = oracle.qk_norm_rope(host(x), n64(w), n64(b), kind, eps, None, None)
+        ref = oracle.qk_norm_rope(host(x), n64(w), n64(b), kind, eps, pos.numpy(), fr.radians.numpy(), **ora)
+        _close(got, ref, np.abs(plain).max(-1, keepdims=True) * fr.magnitude * (4 if kind == "layer" else 1))
+        rx, rw, rb = oracle.qk_norm_rope_grad(host(g), host(x), n64(w), kind, eps, pos.numpy(), fr.radians.numpy(), **ora)
+        xh, r = oracle.qk_norm(host(x), kind, eps)
+        big = np.abs(host(g)).max(-1, keepdims=True) * fr.magnitude
+        size = r * big * np.abs(n64(w)).max()
+        _close(dx, rx, size * (1 + 2 * np.abs(xh).max(-1, keepdims=True)))
+        dy = oracle.rope(host(g), pos.numpy(), fr.radians.numpy(), inverse=True, **ora)
+        # as in test_qk_norm_rope_backward: at most 100 products one after another in a thread
+        tol = 128 * 2.0 ** -24 * np.abs(dy * xh).sum((0, 1, 2)) + 4 * ARITH * (big * np.abs(xh)).sum((0, 1, 2))
+        assert np.all(np.abs(dw.cpu().double().numpy() - rw) <= tol)
+        if kind == "layer":
+            tol = 128 * 2.0 ** -24 * np.abs(dy).sum((0, 1, 2)) + ARITH * (big + 0 * dy).sum((0, 1, 2))
+            assert np.all(np.abs(db.cpu().double().numpy() - rb) <= tol)
+
+
+def test_offsets_past_32_bits():
+    import linear_hybrid_attention_b200 as zb
+    far = 2 ** 31 + 64                                  # elements from one head to the next
+    store = torch.zeros(far + 5 * 64, dtype=torch.bfloat16, device="cuda")
+    view = store.as_strided((1, 2, 5, 64), (0, far, 64, 1))
+    X = _rand((1, 2, 5, 64), 60)
+    view.copy_(X)
+    fr, turns = _freq(zb, 64, 1, "none")
+    pos = _pos(1, 1, 5, 1000, 61).cuda()
+    want = zb.zb_rope(X, pos, turns)
+    assert torch.equal(zb.zb_rope(view, pos, turns), want)
+    q, _ = zb.zb_qk_norm_rope(view, None, pos, turns)
+    q2, _ = zb.zb_qk_norm_rope(X, None, pos, turns)
+    assert torch.equal(q, q2)
+    d = zb.zb_qk_norm_rope_backward(want, None, X, None, pos, turns)
+    zb.zb_qk_norm_rope_backward(want, None, X, None, pos, turns, dQ=view)
+    assert torch.equal(view, d[0])
+    assert zb.zb_rope(view, pos, turns, out=view) is view and torch.equal(view, zb.zb_rope(d[0], pos, turns))
+    sync_ok()
