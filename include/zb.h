@@ -472,7 +472,8 @@ typedef struct zb_rotation {
 } zb_rotation;
 
 /*
- * Y = X rotated (see above); fp32 arithmetic, rounded to bf16 once.  With
+ * Y = X rotated (see above); fp32 arithmetic (sines and cosines of the exactly
+ * reduced angle to 2^-20), rounded to bf16 once; position 0 changes nothing.  With
  * rot.inverse, X the gradient of a forward call's Y gives the gradient of its X.
  *   in : X bf16, rows at x_rows (strides of 0 repeat rows)
  *   out: Y bf16, rows at y_rows (no two of them may overlap).  Y may be X
@@ -610,7 +611,10 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  *   ws : zb_kv8_attn_workspace_bytes() bytes, 16-byte aligned, owned by the
  *        caller and not shared with a call running at the same time
  * fp16 tensor-core products of exact codes, fp32 logits, sums and outputs, O
- * rounded to bf16 once.  The result does not depend on scheduling.
+ * rounded to bf16 once.  The result does not depend on scheduling.  With more than
+ * 32 query rows of a cache head, value scales below 2^-100 count as 2^-100 (values
+ * below 2^-93 may come out as large as that), and a workspace with add_mass holds
+ * one fp32 of every 64 tokens (every block, where smaller) of the slots and row.
  * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0), ZB_ERR_NULL,
  * ZB_ERR_ALIGN, ZB_ERR_UNSUPPORTED (also more than 2^31 - 1 query rows of a cache
  * head), ZB_ERR_WORKSPACE, ZB_ERR_CUDA; ZB_ERR_TIMEOUT in the device status if a

@@ -143,7 +143,7 @@ def zb_kv8_attn(Q, cache: KV8Cache, lens, causal: bool = False, scale: Optional[
     lp = _lens(lens, cache)
     if add_mass and cache.mass is None:
         raise ValueError("add_mass needs a cache with mass")
-    O = _out((heads_q, n_q, d), torch.bfloat16, Q.device, out, "O")
+    O = torch.empty_like(Q) if out is None else _out((heads_q, n_q, d), torch.bfloat16, Q.device, out, "O")
     if want_lse or lse is not None:
         lse = _out((heads_q, n_q), torch.float32, Q.device, lse, "lse")
     key = (heads_q, n_q, add_mass)
@@ -178,8 +178,9 @@ def zb_kv8_evict(table, mass, lens, block: int, budget: int, sinks: int = 0, rec
     budget = int(budget)
     if budget < 1:
         raise ValueError(f"budget must be at least 1, got {budget}")
-    table_out = _out((heads, slots), torch.int32, dev, table_out, "table_out")
-    lens_out = _out((heads,), torch.int32, dev, lens_out, "lens_out")
+    table_out = torch.empty_like(table) if table_out is None else \
+        _out((heads, slots), torch.int32, dev, table_out, "table_out")
+    lens_out = torch.empty_like(lens) if lens_out is None else _out((heads,), torch.int32, dev, lens_out, "lens_out")
     kept = _out((heads, budget), torch.int32, dev, kept, "kept")
     for t, name in ((table_out, "table_out"), (lens_out, "lens_out"), (kept, "kept")):
         if t.device != dev:
