@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
 }
 
 // The weights for more rows (kv8_tile.cu): a warp a block, whose rows' sums are
-// contiguous.  A causal row's sums end where its keys do.
+// contiguous and read in eights.  A causal row's sums end where its keys do; only
+// the last groups have rows that do not see them.
 __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     wait_for_previous();
     const zb_kv8& c = a.c;
@@ -732,11 +733,18 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
         float s = 0.f;
         for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
             const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
-#pragma unroll 4
-            for (int i = lane_id(); i < a.rows; i += 32) {
-                const float t = lse2[i];
-                const bool sees = !a.causal || static_cast<long long>(k) * size < len - a.n_q + 1 + i % a.n_q;
-                if (sees && t != -INFINITY) s += ex2(gs[i] - t);
+            const long long beyond = static_cast<long long>(k) * size - (len - a.n_q);   // of the first query's last key
+            if (!a.causal || beyond <= 0) {
+#pragma unroll 8
+                for (int i = lane_id(); i < a.rows; i += 32) {
+                    const float t = lse2[i], x = ex2(gs[i] - t);
+                    if (t != -INFINITY) s += x;
+                }
+            } else {
+                for (int i = lane_id(); i < a.rows; i += 32) {
+                    const float t = lse2[i];
+                    if (i % a.n_q >= beyond && t != -INFINITY) s += ex2(gs[i] - t);
+                }
             }
         }
 #pragma unroll
