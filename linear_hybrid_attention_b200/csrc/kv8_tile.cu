@@ -24,7 +24,7 @@
 // m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 505 us without weights, 490 TFLOP/s (548 us causal with weights and both
+// tokens: 505 us without weights, 490 TFLOP/s (542 us causal with weights and both
 // joins); 1,280 rows 427 us, 540 TFLOP/s.  A pair of 128 x 128 tiles takes about
 // 3,900 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
 // pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P),
