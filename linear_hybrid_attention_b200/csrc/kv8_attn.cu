@@ -120,7 +120,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
     }
     const long long ctas = min(static_cast<long long>(gridDim.x), total);
     if (blockIdx.x >= ctas) return;
-    const long long at = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+    // (a 64-bit division is some hundred instructions, and the first copy waits for these)
+    auto share = [&](unsigned i) -> long long {
+        if (total < (1 << 24)) return static_cast<uint32_t>(total) * i / static_cast<uint32_t>(ctas);
+        return total * i / ctas;
+    };
+    const long long at = share(blockIdx.x), end = share(blockIdx.x + 1);
     if (before <= at && at < before + mine) {
         long long b = before;
         for (int h = ha; h < hb; ++h) {
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         k.h = h;
         k.len = head_len(a.lens, h, cap);
         k.nc = chunks_of(k.len);
-        k.tile = static_cast<int>(into / (k.nc + 1));
+        k.tile = a.tiles == 1 ? 0 : static_cast<int>(into / (k.nc + 1));
         const int u = static_cast<int>(into - static_cast<long long>(k.tile) * (k.nc + 1));
         const int here = static_cast<int>(min(left, static_cast<long long>(k.nc + 1 - u)));
         k.c0 = max(u - 1, 0);
@@ -161,7 +166,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         return true;
     };
     // this warp's run within the CTA's, and the head it starts in
-    const long long wa = at + (end - at) * warp / WARPS, wb = at + (end - at) * (warp + 1) / WARPS;
+    auto part = [&](int w) -> long long {
+        if (end - at < (1 << 24)) return at + static_cast<uint32_t>(end - at) * w / WARPS;
+        return at + (end - at) * w / WARPS;
+    };
+    const long long wa = part(warp), wb = part(warp + 1);
     if (lane < 2) sm.piece[2 * warp + lane].item = -1;
     Cursor cur, iss;
     bool running = wa < wb;
@@ -538,7 +547,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
             for (; e1 < 2 * WARPS && (sm.piece[e1].item == it || sm.piece[e1].item < 0); ++e1)
                 if (sm.piece[e1].item == it) tail = e1;
         if (it >= 0) {
-            const int h = static_cast<int>(it / a.tiles), row0 = static_cast<int>(it % a.tiles) * TR;
+            const int h = a.tiles == 1 ? static_cast<int>(it) : static_cast<int>(it / a.tiles);
+            const int row0 = static_cast<int>(it - static_cast<long long>(h) * a.tiles) * TR;
             const int live_rows = min(TR, a.rows - row0);
             const long long run = it + blockIdx.x;
             const bool whole = sm.piece[e0].from_start && sm.piece[tail].to_end;
@@ -548,13 +558,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 for (int e = e0; e <= tail; ++e)
                     if (sm.piece[e].item == it) M = fmaxf(M, sm.m[e][r]);
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                 for (int e = e0; e <= tail; ++e) {
-                    if (sm.piece[e].item != it) continue;
-                    const float f = sm.m[e][r] == -INFINITY ? 0.f : ex2(sm.m[e][r] - M);
+                    const bool on = sm.piece[e].item == it;
+                    const float f = !on || sm.m[e][r] == -INFINITY ? 0.f : ex2(sm.m[e][r] - M);
                     const float* src = (e & 1) ? reinterpret_cast<const float*>(&sm.ring[e >> 1][0][0][0])
                                                : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + (e >> 1)) * TR * HD;
-                    const float4 v = *reinterpret_cast<const float4*>(src + r * HD + 4 * q);
-                    L = fmaf(sm.l[e][r], f, L);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (on) v = *reinterpret_cast<const float4*>(src + r * HD + 4 * q);
+                    L = fmaf(on ? sm.l[e][r] : 0.f, f, L);
                     s.x = fmaf(v.x, f, s.x);
                     s.y = fmaf(v.y, f, s.y);
                     s.z = fmaf(v.z, f, s.z);
