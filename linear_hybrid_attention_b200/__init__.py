@@ -341,7 +341,7 @@ def affine_fit_workspace_bytes(heads: int, rows: int, head_dim: int = HEAD_DIM) 
 def _ws(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
     if ws is not None and ws.numel() * ws.element_size() >= nbytes:
         return ws
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    return torch.empty_strided((max(nbytes, 16),), (1,), dtype=torch.uint8, device=device)
 
 
 def zb_linear_state(K, V, S: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,

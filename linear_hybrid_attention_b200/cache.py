@@ -81,7 +81,7 @@ class KV8Cache:
 def _lens(lens, cache: KV8Cache, name: str = "lens") -> int:
     if not isinstance(lens, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if lens.dtype != torch.int32 or tuple(lens.shape) != (cache.heads,) or lens.device != cache.device or \
+    if lens.dtype != torch.int32 or lens.shape != (cache.heads,) or lens.device != cache.device or \
             not lens.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [{cache.heads}] tensor on {cache.device}, "
                          f"got {lens.dtype} {tuple(lens.shape)} on {lens.device}")
@@ -145,7 +145,8 @@ def zb_kv8_attn(Q, cache: KV8Cache, lens, causal: bool = False, scale: Optional[
         raise ValueError("add_mass needs a cache with mass")
     O = torch.empty_like(Q) if out is None else _out((heads_q, n_q, d), torch.bfloat16, Q.device, out, "O")
     if want_lse or lse is not None:
-        lse = _out((heads_q, n_q), torch.float32, Q.device, lse, "lse")
+        lse = torch.empty_strided((heads_q, n_q), (n_q, 1), dtype=torch.float32, device=cache.device) if lse is None \
+            else _out((heads_q, n_q), torch.float32, Q.device, lse, "lse")
     key = (heads_q, n_q, add_mass)
     need = cache._ws_bytes.get(key)
     if need is None:
@@ -181,7 +182,8 @@ def zb_kv8_evict(table, mass, lens, block: int, budget: int, sinks: int = 0, rec
     table_out = torch.empty_like(table) if table_out is None else \
         _out((heads, slots), torch.int32, dev, table_out, "table_out")
     lens_out = torch.empty_like(lens) if lens_out is None else _out((heads,), torch.int32, dev, lens_out, "lens_out")
-    kept = _out((heads, budget), torch.int32, dev, kept, "kept")
+    kept = torch.empty_strided((heads, budget), (budget, 1), dtype=torch.int32, device=dev) if kept is None else \
+        _out((heads, budget), torch.int32, dev, kept, "kept")
     for t, name in ((table_out, "table_out"), (lens_out, "lens_out"), (kept, "kept")):
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}, is on {t.device}")

@@ -82,21 +82,32 @@ def _view(x: torch.Tensor, name: str):
     return b, h, n, _lib.ZbRows(sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
+def _packed(h: int, n: int):
+    """zb_rows of a contiguous [.., h, n, 64] tensor."""
+    return _lib.ZbRows(h * n * HEAD_DIM, n * HEAD_DIM, HEAD_DIM)
+
+
+def _table(t, dtype, ndim: int, name: str, device) -> tuple:
+    """Shape of a contiguous tensor of `ndim` dims on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.dtype != dtype or len(shape) != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {ndim} dims, got {t.dtype} {tuple(shape)}")
+    return shape
+
+
 def _rotation(pos, turns, batch: int, n: int, axes: int, layout: str, magnitude: float, inverse: bool, device):
     if turns is None:
         return _lib.ZbRotation(None, 0, None, 0, 1, 0, 1.0, 0)
-    for t, dt, nd, name in ((pos, torch.int32, 3, "pos"), (turns, torch.int64, 1, "turns")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, is on {t.device}")
-        if t.dtype != dt or t.dim() != nd or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dt} tensor of {nd} dims, got {t.dtype} {tuple(t.shape)}")
-    if pos.shape[0] not in (1, batch) or pos.shape[1] != axes or pos.shape[2] != n:
+    pb, pa, pn = _table(pos, torch.int32, 3, "pos", device)
+    pairs, = _table(turns, torch.int64, 1, "turns", device)
+    if (pb != 1 and pb != batch) or pa != axes or pn != n:
         raise ValueError(f"pos must be [{batch} or 1, {axes}, {n}], got {tuple(pos.shape)}")
-    return _lib.ZbRotation(pos.data_ptr(), axes * n if pos.shape[0] > 1 else 0, turns.data_ptr(),
-                           2 * axes * turns.shape[0], axes, _named(LAYOUTS, layout, "layout"), magnitude,
-                           1 if inverse else 0)
+    return _lib.ZbRotation(pos.data_ptr(), axes * n if pb > 1 else 0, turns.data_ptr(), 2 * axes * pairs, axes,
+                           _named(LAYOUTS, layout, "layout"), magnitude, 1 if inverse else 0)
 
 
 def zb_rope(X, pos, turns, axes: int = 1, layout: str = "half", magnitude: float = 1.0, inverse: bool = False,
@@ -108,12 +119,14 @@ def zb_rope(X, pos, turns, axes: int = 1, layout: str = "half", magnitude: float
     b, h, n, xs = _view(X, "X")
     if out is None:
         out = torch.empty_like(X, memory_format=torch.contiguous_format)
+        ys = _packed(h, n)
     elif out.shape != X.shape or out.device != X.device:
         raise ValueError(f"out must have X's shape and device, got {tuple(out.shape)} on {out.device}")
+    else:
+        ys = _view(out, "out")[3]
     if turns is None:
         raise TypeError("turns must be a torch.Tensor")
     rot = _rotation(pos, turns, b, n, axes, layout, magnitude, inverse, X.device)
-    ys = _view(out, "out")[3]
     _call(X.device, "zb_rope", X.data_ptr(), xs, b, h, n, HEAD_DIM, rot, out.data_ptr(), ys)
     return out
 
@@ -123,7 +136,7 @@ def _feature(t: Optional[torch.Tensor], device, name: str):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.float32 or tuple(t.shape) != (HEAD_DIM,) or t.device != device or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape != (HEAD_DIM,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 [{HEAD_DIM}] tensor on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -194,16 +207,17 @@ def zb_qk_norm_rope_backward(dQo, dKo, Q, K, pos, turns, norm: str = "rms", wq=N
             raise ValueError(f"{name} must be {tuple(x.shape)} on {dev}, got {tuple(g.shape)} on {g.device}")
     dQo = dQo.contiguous()
     dKo = dKo.contiguous() if K is not None else None
+    dqs = _packed(hq, n) if dQ is None else _view(dQ, "dQ")[3]
+    dks = _packed(hk, n) if dK is None or K is None else _view(dK, "dK")[3]
     dQ = _rows_out(Q, dQ, "dQ", False)
     dK = _rows_out(K, dK, "dK", False)
-    zero = _lib.ZbRows(0, 0, 0)
     sums = torch.empty((4, HEAD_DIM), dtype=torch.float32, device=dev)
-    dwq, dwk, dbq, dbk = (sums[i] if on else None for i, on in
-                          enumerate((kind > 0, kind > 0 and hk > 0, kind == 2, kind == 2 and hk > 0)))
+    dwq, dwk, dbq, dbk = (s if on else None for s, on in
+                          zip(sums.unbind(0), (kind > 0, kind > 0 and hk > 0, kind == 2, kind == 2 and hk > 0)))
     ws = _ws(int(_lib_handle().zb_qk_norm_rope_backward_workspace_bytes()), dev, ws)
     if ws.device != dev:
         raise ValueError(f"ws must be on {dev}, is on {ws.device}")
     _call(dev, "zb_qk_norm_rope_backward", dQo.data_ptr(), _ptr(dKo), Q.data_ptr(), qs, hq, _ptr(K), ks, hk, b, n,
-          HEAD_DIM, nm, rot, dQ.data_ptr(), _view(dQ, "dQ")[3], _ptr(dK), zero if dK is None else _view(dK, "dK")[3],
-          _ptr(dwq), _ptr(dwk), _ptr(dbq), _ptr(dbk), ws.data_ptr(), ws.numel() * ws.element_size())
+          HEAD_DIM, nm, rot, dQ.data_ptr(), dqs, _ptr(dK), dks, _ptr(dwq), _ptr(dwk), _ptr(dbq), _ptr(dbk),
+          ws.data_ptr(), ws.numel() * ws.element_size())
     return dQ, dK, dwq, dwk, dbq, dbk
