@@ -158,28 +158,9 @@ ZB_DEVINL uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// A kernel launched behind another one in its stream (launch_behind) starts while
-// that one still runs, and waits here until it is done and its writes are visible.
-ZB_DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-ZB_DEVINL void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ------------------------------------------------------------ host side ----
 // kv8_tile.cu: attention of many rows and the join of its parts (pair: items of 256 rows, else 128).
 zb_status launch_tiles(const AttnArgs& a, bool pair, int ctas, cudaStream_t st);
-
-template <class... P, class... A>
-inline zb_status launch_behind(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
-}
 
 inline zb_status check_cache(const zb_kv8& c, bool codes) {
     if (c.heads < 1 || c.slots < 1) return ZB_ERR_SHAPE;

@@ -882,7 +882,7 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         e = kv8::launch_tiles(a, p.pair, dev.sm_count, st);
         if (e != ZB_OK || !add_mass) return e;
         const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
-        return kv8::launch_behind(kv8::mass_kernel, dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)),
+        return launch_behind(kv8::mass_kernel, dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)),
                                   256, st, a);
     }
     e = cache.format == ZB_KV8_INT8 ? kv8::launch_rows<ZB_KV8_INT8>(a, dev.sm_count, st)
@@ -894,5 +894,5 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         if (parts > 64) parts = 64;
     }
     const dim3 grid(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts));
-    return kv8::launch_behind(p.tile == 8 ? kv8::join_kernel<8> : kv8::join_kernel<kv8::TILE>, grid, 256, st, a);
+    return launch_behind(p.tile == 8 ? kv8::join_kernel<8> : kv8::join_kernel<kv8::TILE>, grid, 256, st, a);
 }

@@ -175,6 +175,7 @@ template <int KIND, bool BACK, bool HALF>
 __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
     constexpr int ROWS = BACK ? 1 : 2;               // worked on together
     constexpr bool NORM = KIND != ZB_NORM_NONE;
+    if (BACK) let_next_start();                      // the sums' kernel, which waits
 
     // the CTA's tensor and its part of that tensor's (group of TOK tokens, head) items
     const bool second = static_cast<int>(blockIdx.x) >= a.side[0].ctas;
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
 // dw and db of one tensor from the CTAs' partial sums, in a fixed order, fp64.
 // Grid: 8 blocks of 8 features x 2 (dw, db) x 2 (queries, keys).
 __global__ void __launch_bounds__(256) reduce_kernel(const float* partial, Args a) {
+    wait_for_previous();
     const int which = blockIdx.y & 1, tensor = blockIdx.y >> 1;
     float* out = which ? a.side[tensor].db : a.side[tensor].dw;
     if (!out) return;
@@ -638,8 +640,7 @@ extern "C" zb_status zb_qk_norm_rope_backward(const uint16_t* dQo, const uint16_
     e = rope::launch<true>(a, norm.kind, dev, st);
     if (e != ZB_OK) return e;
     if (a.side[0].dw || a.side[0].db || a.side[1].dw || a.side[1].db) {
-        rope::reduce_kernel<<<dim3(8, 4), 256, 0, st>>>(a.partial, a);
-        if (cudaGetLastError() != cudaSuccess) return ZB_ERR_CUDA;
+        return launch_behind(rope::reduce_kernel, dim3(8, 4), 256, st, static_cast<const float*>(a.partial), a);
     }
     return ZB_OK;
 }

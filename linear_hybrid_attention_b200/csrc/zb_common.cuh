@@ -367,6 +367,11 @@ ZB_DEVINL float fmax3(float a, float b, float c) {
 ZB_DEVINL float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 ZB_DEVINL float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// A kernel launched behind another one in its stream (launch_behind) starts while
+// that one still runs, and waits here until it is done and its writes are visible.
+ZB_DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+ZB_DEVINL void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 ZB_DEVINL int warp_id() { return threadIdx.x >> 5; }
 ZB_DEVINL int lane_id() { return threadIdx.x & 31; }
 

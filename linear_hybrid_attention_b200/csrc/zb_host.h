@@ -27,6 +27,22 @@ unsigned long long wait_timeout_ns();
 zb_status make_map_bf16_3d(CUtensorMap* map, const void* base, int inner, long long rows,
                            int outer, int box_rows);
 
+// A launch that may start before the kernel in front of it is done; it waits for it with
+// wait_for_previous.
+template <class... P, class... A>
+inline zb_status launch_behind(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? ZB_OK : ZB_ERR_CUDA;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline long long n_tiles(const zb_shape& s) { return (s.n_tokens + s.tile - 1) / s.tile; }
