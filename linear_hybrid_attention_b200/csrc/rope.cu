@@ -130,12 +130,12 @@ ZB_DEVINL float row_sum(float v) {   // over the row's four lanes
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// (x, y) by the angle of (c, s): x c - y s, y c + x s, with -s given beside s.
-ZB_DEVINL void rotate(f2* v, const f2* c, const f2* s, const f2* ns) {
+// (x, y) by the angle of (c, s): x c - y s, y c + x s.
+ZB_DEVINL void rotate(f2* v, const f2* c, const f2* s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const f2 x = v[i], y = v[4 + i];
-        v[i] = f2_fma(x, c[i], f2_mul(y, ns[i]));
+        v[i] = f2_sub(f2_mul(x, c[i]), f2_mul(y, s[i]));
         v[4 + i] = f2_fma(y, c[i], f2_mul(x, s[i]));
     }
 }
@@ -173,7 +173,7 @@ constexpr int CTAS = 2;                // an SM: 128 registers a thread; with 80
 
 template <int KIND, bool BACK, bool HALF>
 __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
-    constexpr int ROWS = BACK ? 1 : 2;               // worked on together
+    constexpr int ROWS = BACK ? 1 : 2;               // under way; forward they are worked on together
     constexpr bool NORM = KIND != ZB_NORM_NONE;
     if (BACK) let_next_start();                      // the sums' kernel, which waits
 
@@ -239,25 +239,22 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
         const uint4* g = BACK ? reinterpret_cast<const uint4*>(sd.g + b * sd.gs.b + t * sd.gs.t + h0 * sd.gs.h) : nullptr;
         uint4* o = reinterpret_cast<uint4*>(sd.out + b * sd.os.b + t * sd.os.t + h0 * sd.os.h);
         // the next ROWS rows are on their way while these are worked on
-        uint4 xv[ROWS][2], gv[2];
-        auto load = [&](int r) {
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k) {
-                if (k == 0 || r + k < n) {           // otherwise an old row again, not stored
-                    xv[k][0] = __ldg(x + c0);
-                    xv[k][1] = __ldg(x + c1);
-                    x += xh;
-                }
-            }
+        uint4 xv[ROWS][2], gv[BACK ? ROWS : 1][2];
+        auto load = [&](int k) {
+            xv[k][0] = __ldg(x + c0);
+            xv[k][1] = __ldg(x + c1);
+            x += xh;
             if (BACK) {
-                gv[0] = live ? __ldg(g + c0) : make_uint4(0, 0, 0, 0);
-                gv[1] = live ? __ldg(g + c1) : make_uint4(0, 0, 0, 0);
+                gv[k][0] = live ? __ldg(g + c0) : make_uint4(0, 0, 0, 0);
+                gv[k][1] = live ? __ldg(g + c1) : make_uint4(0, 0, 0, 0);
                 g += gh;
             }
         };
 #pragma unroll
-        for (int k = 1; k < ROWS; ++k) xv[k][0] = xv[k][1] = make_uint4(0, 0, 0, 0);
-        load(0);
+        for (int k = 0; k < ROWS; ++k) {
+            xv[k][0] = xv[k][1] = make_uint4(0, 0, 0, 0);
+            if (k == 0 || k < n) load(k);            // a row that is not there: zeros, then an old row again, not stored
+        }
         // forward, a row is r (x w c - y w' s) + b: weights and biases turned once a token
         f2 ca[4], cb[4], sa[4], sb[4], z[8];
         {
@@ -288,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
                     z[4 + i] = bias(4 + i);
                 }
             }
-            if (!BACK && KIND == ZB_NORM_LAYER && turned) rotate(z, ca, sa, sb);
+            if (!BACK && KIND == ZB_NORM_LAYER && turned) rotate(z, ca, sa);
             if (!BACK && NORM) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -303,16 +300,25 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
 #pragma unroll 1
         for (int r = 0; r < n; r += ROWS) {
             f2 f[ROWS][8], e[8];
+            if (!BACK) {
 #pragma unroll
-            for (int k = 0; k < ROWS; ++k) unpack<HALF>(xv[k][0], xv[k][1], f[k]);
-            if (BACK) unpack<HALF>(gv[0], gv[1], e);
-            if (r + ROWS < n) load(r + ROWS);
+                for (int k = 0; k < ROWS; ++k) unpack<HALF>(xv[k][0], xv[k][1], f[k]);
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k)
+                    if (r + ROWS + k < n) load(k);
+            }
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
+                if (BACK) {
+                    if (k && r + k >= n) break;
+                    unpack<HALF>(xv[k][0], xv[k][1], f[k]);
+                    unpack<HALF>(gv[BACK ? k : 0][0], gv[BACK ? k : 0][1], e);
+                    if (r + ROWS + k < n) load(k);
+                }
                 const float inv = centre<KIND>(f[k], a.eps);
                 const f2 inv2 = f2_pack(inv, inv);
                 if (BACK) {
-                    if (turned) rotate(e, ca, sa, sb);
+                    if (turned) rotate(e, ca, sa);
                     f2 t1 = 0ull, t0 = 0ull;
                     if (NORM) {
 #pragma unroll
