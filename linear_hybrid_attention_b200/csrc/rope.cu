@@ -171,10 +171,15 @@ ZB_DEVINL void sincos_turns(int frac, float& sn, float& cs) {
 
 constexpr int CTAS = 2;                // an SM: 128 registers a thread; with 80 (three) most kernels spill
 
+ZB_DEVINL void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int KIND, bool BACK, bool HALF>
 __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
     constexpr int ROWS = BACK ? 1 : 2;               // under way; forward they are worked on together
     constexpr bool NORM = KIND != ZB_NORM_NONE;
+    // the next group's first rows go to L2 and its position to a register while a group is worked on
+    // (rms norm of 16 + 4 heads 24 -> 21 us); the layer norm has no register left for it (67 -> 69)
+    constexpr bool AHEAD = KIND != ZB_NORM_LAYER;
     if (BACK) let_next_start();                      // the sums' kernel, which waits
 
     // the CTA's tensor and its part of that tensor's (group of TOK tokens, head) items
@@ -225,6 +230,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
     }
 
     const long long xh = sd.xs.h / 8, gh = sd.gs.h / 8, oh = sd.os.h / 8;
+    int pos_ahead = 0;
+    bool ahead = false;
 #pragma unroll 1
     while (left > 0) {
         const int n = heads - h0 < left ? heads - h0 : static_cast<int>(left);   // rows of this group
@@ -255,6 +262,19 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
             xv[k][0] = xv[k][1] = make_uint4(0, 0, 0, 0);
             if (k == 0 || k < n) load(k);            // a row that is not there: zeros, then an old row again, not stored
         }
+        if (AHEAD && left > n && live && t + TOK < a.n) {
+            const uint4* xn = reinterpret_cast<const uint4*>(sd.x + b * sd.xs.b + (t + TOK) * sd.xs.t);
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                prefetch_l2(xn + k * xh + c0);
+                prefetch_l2(xn + k * xh + c1);
+            }
+            if (BACK) {
+                const uint4* gn = reinterpret_cast<const uint4*>(sd.g + b * sd.gs.b + (t + TOK) * sd.gs.t);
+                prefetch_l2(gn + c0);
+                prefetch_l2(gn + c1);
+            }
+        }
         // forward, a row is r (x w c - y w' s) + b: weights and biases turned once a token
         f2 ca[4], cb[4], sa[4], sb[4], z[8];
         {
@@ -265,7 +285,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
                 s[j] = 0.f;
             }
             if (turned) {
-                const unsigned long long pos = static_cast<long long>(__ldg(a.pos + b * a.pos_b + axis * a.n + t));
+                const int32_t* at = a.pos + b * a.pos_b + axis * a.n + t;
+                const unsigned long long pos = static_cast<long long>(ahead ? pos_ahead : __ldg(at));
+                ahead = AHEAD && t + TOK < a.n;
+                if (ahead) pos_ahead = __ldg(at + TOK);
                 const float way = BACK || a.inverse ? -a.mag : a.mag;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
