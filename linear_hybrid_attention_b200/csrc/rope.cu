@@ -28,7 +28,7 @@
 //
 // Measured (B200): rotation alone, 16 heads of 43,968 tokens, 32 us (27 at the
 // copy rate); layer norm and rotation of 16 + 16 heads of 43,968 tokens 67 us
-// (54); rms norm of 16 + 4 heads of 2 x 10,992 tokens 24 us forward, 40 + 3
+// (54); rms norm of 16 + 4 heads of 2 x 10,992 tokens 21 us forward, 39 + 3
 // backward (17 and 25).  Before: scalar arithmetic, weights in registers and
 // sincospi 37, 83, 32 and 48 + 6 us; rows copied ahead through shared memory
 // instead of registers 38, 98, 35 and 57 (the shared memory's own bandwidth);
