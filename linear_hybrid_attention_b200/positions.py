@@ -153,6 +153,17 @@ def _pair(Q, K):
     return b, hq, hk, n, qs, ks
 
 
+def _gradient(g, x, name: str) -> torch.Tensor:
+    """g, the gradient of an output of x's shape, contiguous."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if g.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {g.dtype}")
+    if g.shape != x.shape or g.device != x.device:
+        raise ValueError(f"{name} must be {tuple(x.shape)} on {x.device}, got {tuple(g.shape)} on {g.device}")
+    return g.contiguous()
+
+
 def _rows_out(like, out: Optional[torch.Tensor], name: str, contiguous: bool):
     """An output of `like`'s shape; a given one must match (and be contiguous where the call wants it)."""
     if like is None:
@@ -199,25 +210,33 @@ def zb_qk_norm_rope_backward(dQo, dKo, Q, K, pos, turns, norm: str = "rms", wq=N
     kind = _named(NORMS, norm, "norm")
     rot = _rotation(pos, turns, b, n, axes, layout, magnitude, False, dev)
     nm = _lib.ZbQkNorm(kind, eps, _feature(wq, dev, "wq"), _feature(wk, dev, "wk"), None, None)
-    for g, x, name in ((dQo, Q, "dQo"), (dKo, K, "dKo")):
-        if x is None:
-            continue
-        _view(g, name)
-        if g.shape != x.shape or g.device != dev:
-            raise ValueError(f"{name} must be {tuple(x.shape)} on {dev}, got {tuple(g.shape)} on {g.device}")
-    dQo = dQo.contiguous()
-    dKo = dKo.contiguous() if K is not None else None
-    dqs = _packed(hq, n) if dQ is None else _view(dQ, "dQ")[3]
-    dks = _packed(hk, n) if dK is None or K is None else _view(dK, "dK")[3]
-    dQ = _rows_out(Q, dQ, "dQ", False)
-    dK = _rows_out(K, dK, "dK", False)
-    sums = torch.empty((4, HEAD_DIM), dtype=torch.float32, device=dev)
-    dwq, dwk, dbq, dbk = (s if on else None for s, on in
-                          zip(sums.unbind(0), (kind > 0, kind > 0 and hk > 0, kind == 2, kind == 2 and hk > 0)))
-    ws = _ws(int(_lib_handle().zb_qk_norm_rope_backward_workspace_bytes()), dev, ws)
+    dQo = _gradient(dQo, Q, "dQo")
+    if dQ is None:
+        dQ, dqs = torch.empty_like(Q, memory_format=torch.contiguous_format), _packed(hq, n)
+    else:
+        dqs = _view(_rows_out(Q, dQ, "dQ", False), "dQ")[3]
+    dks = ks
+    if K is None:
+        dKo = dK = None
+    else:
+        dKo = _gradient(dKo, K, "dKo")
+        if dK is None:
+            dK, dks = torch.empty_like(K, memory_format=torch.contiguous_format), _packed(hk, n)
+        else:
+            dks = _view(_rows_out(K, dK, "dK", False), "dK")[3]
+    dwq = dwk = dbq = dbk = None
+    if kind:
+        rows = torch.empty_strided((4, HEAD_DIM), (HEAD_DIM, 1), dtype=torch.float32, device=dev)
+        if kind == 1:
+            dwq, dwk = rows[0], rows[1] if hk else None
+        else:
+            dwq, dwk, dbq, dbk = rows.unbind(0)
+            if not hk:
+                dwk = dbk = None
+    ws = _ws(_lib_handle().zb_qk_norm_rope_backward_workspace_bytes(), dev, ws)
     if ws.device != dev:
         raise ValueError(f"ws must be on {dev}, is on {ws.device}")
     _call(dev, "zb_qk_norm_rope_backward", dQo.data_ptr(), _ptr(dKo), Q.data_ptr(), qs, hq, _ptr(K), ks, hk, b, n,
           HEAD_DIM, nm, rot, dQ.data_ptr(), dqs, _ptr(dK), dks, _ptr(dwq), _ptr(dwk), _ptr(dbq), _ptr(dbk),
-          ws.data_ptr(), ws.numel() * ws.element_size())
+          ws.data_ptr(), ws.nbytes)
     return dQ, dK, dwq, dwk, dbq, dbk
