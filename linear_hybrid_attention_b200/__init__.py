@@ -36,7 +36,9 @@ HEAD_DIM = 64
 
 # kernels each entry point launches (for counting launches in a timed region);
 # zb_tile_score_topk launches 4 per pass over the heads its workspace holds
-# (topk_launches gives the count of one call)
+# (topk_launches gives the count of one call), zb_kv8_attn one more with add_mass and
+# more than 32 query rows of a cache head, zb_kv8_append one more where it advances
+# lengths in place over several units of rows
 LAUNCHES_PER_CALL = {
     "zb_landmark_build": 1, "zb_tile_score_topk": 4, "zb_tile_sparse_attn": 1, "zb_dense_attn": 1,
     "zb_dense_attn_split": 2,

@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
             const uint4* xn = reinterpret_cast<const uint4*>(sd.x + b * sd.xs.b + (t + TOK) * sd.xs.t);
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
+                if (k >= heads) break;
                 prefetch_l2(xn + k * xh + c0);
                 prefetch_l2(xn + k * xh + c1);
             }
