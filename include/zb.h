@@ -611,7 +611,10 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  *   ws : zb_kv8_attn_workspace_bytes() bytes, 16-byte aligned, owned by the
  *        caller and not shared with a call running at the same time
  * fp16 tensor-core products of exact codes, fp32 logits, sums and outputs, O
- * rounded to bf16 once.  The result does not depend on scheduling.  With more than
+ * rounded to bf16 once.  A softmax weight enters the products as fp16: rounded to
+ * 2^-11 of itself, and by up to 2^-39 of the row's largest where it is below 2^-28
+ * of that (2^-32 and 2^-21 with more than 32 query rows of a cache head); sums, lse
+ * and mass take it unrounded.  The result does not depend on scheduling.  With more than
  * 32 query rows of a cache head, value scales below 2^-100 count as 2^-100 (values
  * below 2^-93 may come out as large as that), and a workspace with add_mass holds
  * one fp32 of every 64 tokens (every block, where smaller) of the slots and row.
