@@ -108,6 +108,18 @@ ZB_DEVINL void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
         : "memory");
 }
 
+// mbar_wait_warp for phases that cannot come round again before this warp arrives: most are
+// there already, and then one vote answers, without a branch that lanes could part at.
+ZB_DEVINL bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, w);
+}
+ZB_DEVINL bool wait_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, const WaitCtx& w) {
+    const bool first = mbar_try_wait(bar0, parity0), second = mbar_try_wait(bar1, parity1);
+    if (__all_sync(0xffffffffu, first && second)) return true;
+    return mbar_wait_warp(bar0, parity0, w) && mbar_wait_warp(bar1, parity1, w);
+}
+
 // Instruction descriptor: fp16 A and B, fp32 accumulator (b_mn: B stored along N).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
     return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             bool ok = true, held = false;                      // scales read and not yet put
             float ks = 0.f, vs = 0.f;
             auto put_scales = [&]() -> bool {                  // of the tile before
-                if (!mbar_wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc)) return false;
+                if (!wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc)) return false;
                 const bool bad = !(fabsf(vs) <= 3.4e38f);
                 // codes under a zero scale are zeros: any scale does, and 1 keeps -inf * s_k what it is.
                 // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
@@ -311,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     int slot = 0;
                     if (lane < have) slot = slot_of(c, walk.h, (key0 + lane * piece_rows) >> shift, a.status);
                     if (held && !(ok = put_scales())) break;
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_empty[raw.st]), raw.ph ^ 1u, wc))) break;
+                    if (!(ok = wait_warp(smem_addr(&sm.raw_empty[raw.st]), raw.ph ^ 1u, wc))) break;
                     const uint32_t bar = smem_addr(&sm.raw_full[raw.st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have) * 2 * piece_bytes);
                     __syncwarp();
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         bool ok = true;
         for (; running && ok; running = items.next(walk)) {
             for (int t = walk.c0; t < walk.c1; ++t) {
-                if (!(ok = mbar_wait_warp(smem_addr(&sm.raw_full[raw.st]), raw.ph, wc))) break;
+                if (!(ok = wait_warp(smem_addr(&sm.raw_full[raw.st]), raw.ph, wc))) break;
                 const uint8_t* src = sm.raw[raw.st][which];
                 uint4 w[8];
 #pragma unroll
@@ -444,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[raw.st]));
                 raw.step();
-                if (!(ok = mbar_wait_warp(smem_addr(empty + to.st), to.ph ^ 1u, wc))) break;
+                if (!(ok = wait_warp(smem_addr(empty + to.st), to.ph ^ 1u, wc))) break;
                 uint8_t* dst = tiles + to.st * TILE_BYTES;
                 // values behind the last token must be finite: what the ring holds there is anything
                 const int valid = which ? min(walk.len - t * BN, BN) : BN;
@@ -529,8 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 for (int j = j0; j < n; j += STEP, ++g) {
                     const uint32_t t = base + j;
                     const int sc = t % SC;
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.s_full[s]), g & 1, wc))) break;
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.sc_full[sc]), (t / SC) & 1, wc))) break;
+                    if (!(ok = wait_warp(smem_addr(&sm.s_full[s]), g & 1, smem_addr(&sm.sc_full[sc]), (t / SC) & 1, wc))) break;
                     tc_fence_after();
                     const int seen = max(min(lim - (walk.c0 + j) * BN, BN), 0);
                     float alpha = 1.f, nm = 0.f, weight = 0.f;
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         }
                         nm = (m == -INFINITY ? 0.f : -m) + SHIFT;
                         // P is free once P V of the step before is done; O then holds every earlier step
-                        if (!mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc)) return false;
+                        if (!wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc)) return false;
                         tc_fence_after();
                         exponentials(1, x);
                         load(0, x);
@@ -647,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 }
                 if (!ok) break;
                 // the last P V
-                if (!(ok = mbar_wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
+                if (!(ok = wait_warp(smem_addr(&sm.p_free[s]), (g & 1) ^ 1, wc))) break;
                 tc_fence_after();
             }
             base += n;
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             if (!PAIR) {
                 // the slots hold the same rows: slot 1 hands its sums to slot 0
                 if (s == 1) {
-                    if (!(ok = mbar_wait_warp(smem_addr(&sm.other_empty), (part & 1) ^ 1, wc))) break;
+                    if (!(ok = wait_warp(smem_addr(&sm.other_empty), (part & 1) ^ 1, wc))) break;
 #pragma unroll
                     for (int i = 0; i < HD / 4; ++i)
                         sm.other[i][row] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     mbar_arrive(smem_addr(&sm.other_full));
                     continue;
                 }
-                if (!(ok = mbar_wait_warp(smem_addr(&sm.other_full), part & 1, wc))) break;
+                if (!(ok = wait_warp(smem_addr(&sm.other_full), part & 1, wc))) break;
                 const float2 ml = sm.other_ml[row];
                 const float M = fmaxf(m, ml.x);
                 const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
