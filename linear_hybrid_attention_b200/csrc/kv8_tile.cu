@@ -24,13 +24,15 @@
 // m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 505 us without weights, 490 TFLOP/s (542 us causal with weights and both
-// joins); 1,280 rows 427 us, 540 TFLOP/s.  A pair of 128 x 128 tiles takes about
-// 3,900 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
-// pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P),
-// which the other slot's warp covers only in part.  Also built, and slower by 2 to
-// 20%: three slots of 64 keys; four slots of 64 keys with P in S's columns; the two
-// slots' exponentials taking turns (a hand-over costs what it saves).
+// tokens: 462 us without weights, 535 TFLOP/s (538 us causal with weights and both
+// joins); 1,280 rows 387 us, 595 TFLOP/s.  A pair of 128 x 128 tiles takes about
+// 3,500 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
+// pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P, and
+// waits of some 150 cycles each even where the phase is there: answering them by one
+// vote took 507 us to 462), which the other slot's warp covers only in part.  Also
+// built, and slower by 2 to 20%: three slots of 64 keys; four slots of 64 keys with P
+// in S's columns; the two slots' exponentials taking turns (a hand-over costs what it
+// saves); P V in halves under the other half's exponentials.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
