@@ -24,8 +24,8 @@
 // m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 462 us without weights, 535 TFLOP/s (538 us causal with weights and both
-// joins); 1,280 rows 387 us, 595 TFLOP/s.  A pair of 128 x 128 tiles takes about
+// tokens: 460 us without weights, 538 TFLOP/s (535 us causal with weights and both
+// joins); 1,280 rows 386 us, 597 TFLOP/s.  A pair of 128 x 128 tiles takes about
 // 3,500 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
 // pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P, and
 // waits of some 150 cycles each even where the phase is there: answering them by one
@@ -641,8 +641,6 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         return true;
                     };
                     if (!(ok = __any_sync(0xffffffffu, seen < BN) ? step(std::true_type{}) : step(std::false_type{}))) break;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
                     if (__any_sync(0xffffffffu, raise && j > j0)) {
                         const float al = raise && j > j0 ? alpha : 1.f;
                         uint32_t ro[HD];
@@ -653,6 +651,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     tc_fence_before();
                     mbar_arrive(smem_addr(&sm.p_full[s]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc]));
                     if (MASS) {                                      // past this tile, and the other slot's
                         gsum += static_cast<long long>(per_tile) * STEP * a.rows;
                         gsum_left -= per_tile * STEP;
