@@ -728,10 +728,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     }
 }
 
-// The weights for more rows (kv8_tile.cu): a CTA a block, whose rows' sums are
-// contiguous; a thread has its rows of a group under way together (a warp a block, in
-// eights, took 25 us for 60 MB of sums).  A causal row's sums end where its keys do;
-// only the last groups have rows that do not see them.
+// The weights for more rows (kv8_tile.cu): a warp a block, whose rows' sums are
+// contiguous and read in eights.  A causal row's sums end where its keys do; only
+// the last groups have rows that do not see them.
 __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     wait_for_previous();
     const zb_kv8& c = a.c;
@@ -742,21 +741,19 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
     const int live = static_cast<int>((len + min(c.block, CHUNK) - 1) / min(c.block, CHUNK));
     const int size = min(c.block, CHUNK);
     const float* lse2 = a.lse2 + static_cast<long long>(h) * a.rows;
-    __shared__ float red[2][8];
-    int turn = 0;
-    for (int b = blockIdx.y; b < blocks; b += gridDim.y, turn ^= 1) {
+    for (int b = blockIdx.y * 8 + warp_id(); b < blocks; b += gridDim.y * 8) {
         float s = 0.f;
         for (int k = b * per_block; k < min((b + 1) * per_block, live); ++k) {
             const float* gs = a.gsum + (static_cast<long long>(h) * a.groups + k) * a.rows;
             const long long beyond = static_cast<long long>(k) * size - (len - a.n_q);   // of the first query's last key
             if (!a.causal || beyond <= 0) {
 #pragma unroll 8
-                for (int i = threadIdx.x; i < a.rows; i += 256) {
+                for (int i = lane_id(); i < a.rows; i += 32) {
                     const float t = lse2[i], x = ex2(gs[i] - t);
                     if (t != -INFINITY) s += x;
                 }
             } else {
-                for (int i = threadIdx.x; i < a.rows; i += 256) {
+                for (int i = lane_id(); i < a.rows; i += 32) {
                     const float t = lse2[i];
                     if (i % a.n_q >= beyond && t != -INFINITY) s += ex2(gs[i] - t);
                 }
@@ -764,11 +761,7 @@ __global__ void __launch_bounds__(256) mass_kernel(const AttnArgs a) {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane_id() == 0) red[turn][warp_id()] = s;
-        __syncthreads();                             // (two places in turn: one barrier a block)
-        if (threadIdx.x == 0) {
-            s = 0.f;
-            for (int w = 0; w < 8; ++w) s += red[turn][w];
+        if (lane_id() == 0) {
             const int slot = slot_of(c, h, b, a.status);
             c.mass[static_cast<long long>(h) * c.slots + slot] += s;
         }
@@ -888,7 +881,7 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
         if (add_mass) a.lse2 = reinterpret_cast<float*>(w + p.o + p.ml + p.item + p.gsum);
         e = kv8::launch_tiles(a, p.pair, dev.sm_count, st);
         if (e != ZB_OK || !add_mass) return e;
-        const int parts = cache.slots < 512 ? cache.slots : 512;
+        const int parts = cache.slots / 8 + 1 < 512 ? cache.slots / 8 + 1 : 512;
         return launch_behind(kv8::mass_kernel, dim3(static_cast<unsigned>(cache.heads), static_cast<unsigned>(parts)),
                                   256, st, a);
     }
