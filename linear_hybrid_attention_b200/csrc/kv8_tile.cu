@@ -306,9 +306,12 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             auto put_scales = [&]() -> bool {                  // of the tile before
                 if (!wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc)) return false;
                 const bool bad = !(fabsf(vs) <= 3.4e38f);
-                // codes under a zero scale are zeros: any scale does, and 1 keeps -inf * s_k what it is.
+                // codes under a zero scale are zeros: any scale does for the product, but the softmax's reference
+                // takes it as well, so a block of zeros counts as one of the smallest values (as 1 it pushed the
+                // other blocks' weights out of fp16).  A scale that is not finite has a path of its own, and 1
+                // keeps -inf * s_k what it is.
                 // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
-                const float v = bad || vs == 0.f ? 1.f : fmaxf(vs, 0x1p-100f);
+                const float v = bad ? 1.f : fmaxf(vs, 0x1p-100f);
                 const float lv = log2f(v);
                 if (lane < G) sm.sc[sc.st][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
                 const uint32_t nan = __ballot_sync(0xffffffffu, lane < G && bad);
