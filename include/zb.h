@@ -613,11 +613,13 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  * fp16 tensor-core products of exact codes, fp32 logits, sums and outputs, O
  * rounded to bf16 once.  A softmax weight enters the products as fp16: rounded to
  * 2^-11 of itself, and by up to 2^-39 of the row's largest where it is below 2^-28
- * of that (2^-32 and 2^-21 with more than 32 query rows of a cache head); sums, lse
- * and mass take it unrounded.  The result does not depend on scheduling.  With more than
- * 32 query rows of a cache head, value scales below 2^-100 count as 2^-100 (values
- * below 2^-93 may come out as large as that), and a workspace with add_mass holds
- * one fp32 of every 64 tokens (every block, where smaller) of the slots and row.
+ * of that (2^-31 and 2^-20 with more than 32 query rows of a cache head); sums, lse
+ * and mass take it unrounded, and do not depend on the values.  The result does not
+ * depend on scheduling.  With more than 32 query rows of a cache head, blocks whose
+ * value scale is below 2^-24 (int8; e4m3: 2^-15) of the largest of their head lose
+ * bits of their weights, and below 2^-40 (2^-31) may count as zeros; and a workspace
+ * with add_mass holds one fp32 of every 64 tokens (every block, where smaller) of
+ * the slots and row.
  * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0), ZB_ERR_NULL,
  * ZB_ERR_ALIGN, ZB_ERR_UNSUPPORTED (also more than 2^31 - 1 query rows of a cache
  * head), ZB_ERR_WORKSPACE, ZB_ERR_CUDA; ZB_ERR_TIMEOUT in the device status if a

@@ -70,12 +70,18 @@ ZB_DEVINL uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
-ZB_DEVINL uint32_t sub_1152(uint32_t h2) {
+ZB_DEVINL uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    // as 1 x - 1152: exact as well, and half the latency of a subtraction here
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(h2), "r"(0x3C003C00u), "r"(0xE480E480u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+ZB_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 1 x - 1152: exact, and half the latency of a subtraction here.
+ZB_DEVINL uint32_t sub_1152(uint32_t h2) { return fma_f16x2(h2, 0x3C003C00u, 0xE480E480u); }
 template <>
 ZB_DEVINL void unpack4<ZB_KV8_INT8>(uint32_t w, uint32_t& lo, uint32_t& hi) {
     w ^= 0x80808080u;
@@ -88,6 +94,14 @@ ZB_DEVINL void unpack4<ZB_KV8_E4M3>(uint32_t w, uint32_t& lo, uint32_t& hi) {
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
+}
+
+// Int8 codes times a power of two (a pair of fp16) that leaves them, and 1152, exact.
+ZB_DEVINL void unpack4_int8(uint32_t w, uint32_t mul, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    const uint32_t off = mul_f16x2(mul, 0xE480E480u);        // -1152
+    lo = fma_f16x2(prmt(w, 0x64646464u, 0x4140u), mul, off);
+    hi = fma_f16x2(prmt(w, 0x64646464u, 0x4342u), mul, off);
 }
 
 ZB_DEVINL float2 half2_floats(uint32_t h2) { return __half22float2(*reinterpret_cast<const __half2*>(&h2)); }

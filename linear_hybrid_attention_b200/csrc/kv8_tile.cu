@@ -4,8 +4,8 @@
 // The same mathematics as kv8_attn.cu, bound by the exponentials and the
 // instructions around them rather than by the cache's bytes.  One persistent CTA
 // per SM, 512 threads:
-//   warp 0        loader: bulk copies of a 128-key tile's codes into a ring, and
-//                 the tile's scales
+//   warp 0        loader: bulk copies of a 128-key tile's codes into a ring
+//   warp 3        the tiles' scales, up to eight tiles ahead
 //   warps 1, 2    MMA issuers of row tiles ("slots") 0 and 1: S = Q K^T, O += P V
 //   warps 4..7    converters (two for K, two for V): codes to fp16, exactly, in the
 //                 128-byte-swizzle layout the MMAs read
@@ -18,14 +18,21 @@
 // less than an item: those go to the workspace, to the CTA's two places there, and a
 // second kernel adds them up.
 //
-// Scales.  s_k multiplies the logits, 64 or 16 columns at a time.  s_v rides in the
-// exponent: P = 2^(x + log2 s_v - m), so that O += P code needs no further product,
-// and the softmax sum takes those columns' sum of P times 1 / s_v.  The running reference
-// m is the maximum of x + log2 s_v, raised only when it grows by more than RAISE.
+// Scales.  s_k multiplies the logits, 64 or 16 columns at a time.  s_v = f 2^e, 1/2 <= f < 1:
+// 2^(e - r) goes into the converted values, which it leaves exact, and f into the
+// exponent, P = 2^(x + log2 f - m), so that O += P V needs no further product, and the
+// softmax sum takes those columns' sum of P times 1 / f.  r is the part's reference for its
+// values, the e of its first block that is not all zeros, raised where a block is 2^K_MAX
+// larger; O is multiplied by 2^-(what it grew by) then.  So fp16 holds a weight relative to
+// its row's largest weight, whatever the values' sizes.  (With all of s_v in the exponent it
+// held weight times scale relative to the largest such product: a block of large values
+// that had most of a row's weight took the bits of all others.)  m is the running maximum
+// of x, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 460 us without weights, 538 TFLOP/s (535 us causal with weights and both
-// joins); 1,280 rows 386 us, 597 TFLOP/s.  A pair of 128 x 128 tiles takes about
+// tokens: 475 us without weights, 521 TFLOP/s (533 us causal with weights and both
+// joins); 1,280 rows 400 us, 576 TFLOP/s; e4m3 in blocks of 16, 1,374 rows 500 us.  Of
+// that the powers of two in the values cost 3 to 6% without weights, nothing with them.  A pair of 128 x 128 tiles takes about
 // 3,500 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
 // pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P, and
 // waits of some 150 cycles each even where the phase is there: answering them by one
@@ -47,7 +54,7 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int THREADS = 512;
-constexpr int RAW = 3, K16 = 3, V16 = 3, SC = 4;   // ring stages
+constexpr int RAW = 3, K16 = 3, V16 = 3, SC = 8;   // ring stages
 constexpr uint32_t RAW_BYTES = BN * HD;            // 8 KB of codes
 constexpr uint32_t TILE_BYTES = BN * HD * 2;       // 16 KB of fp16
 constexpr uint32_t TMEM_COLS = 512, SLOT_COLS = 256, TM_S = 0, TM_P = 128, TM_O = 192;
@@ -55,9 +62,22 @@ constexpr uint32_t SLEEP_NS = 20000;
 // 128 threads each of roles and converters, 256 of softmax; adds up to the launch's 512 x 128
 constexpr int LAUNCH_REGS = 128, ROLE_REGS = 64, CONVERT_REGS = 96, SOFTMAX_REGS = 176;
 static_assert(128 * (ROLE_REGS + CONVERT_REGS) + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
-// P is at most 2^(SHIFT + RAISE) in fp16 and rounded to 2^-11 of its value down to
-// 2^-(SHIFT + 14) of the reference, to 2^-(SHIFT + 25) of it below.
+// P is at most 2^(SHIFT + RAISE) in fp16, and a row's largest weight at least 2^(SHIFT - 1):
+// weights are rounded to 2^-11 of themselves down to 2^-(SHIFT + 13) of the largest, to
+// 2^-(SHIFT + 24) of it below.
 constexpr float SHIFT = 7.f, RAISE = 8.f;
+// Powers of two that a format's codes can be multiplied by in fp16: up to the largest value,
+// and down to where the smallest step of a code is fp16's smallest number.  (1152 as well,
+// which the conversion of int8 multiplies.)  Scales below K_MIN take up to K_REST of what is
+// missing off the weights, where fp16 then loses bits; a block below that counts as zeros.
+template <int FMT>
+constexpr int K_MAX = FMT == ZB_KV8_INT8 ? 5 : 7;
+template <int FMT>
+constexpr int K_MIN = FMT == ZB_KV8_INT8 ? -24 : -15;
+constexpr int K_REST = 16;
+constexpr int NO_REF = -126;      // of a part without values yet: the smallest exponent of a scale
+ZB_DEVINL uint32_t ref_word(int ref) { return static_cast<uint32_t>(ref + 256) << 8; }
+ZB_DEVINL int word_ref(uint32_t word) { return static_cast<int>(word >> 8) - 256; }
 
 struct __align__(1024) TileSmem {
     uint8_t q[2][TILE_BYTES];
@@ -66,8 +86,9 @@ struct __align__(1024) TileSmem {
     uint8_t raw[RAW][2][RAW_BYTES];
     float4 other[HD / 4][BM];         // slot 1's sums where it shares slot 0's rows
     float2 other_ml[BM];
-    float4 sc[SC][8];                 // s_k, log2 s_v, 1 / s_v of 64 or 16 keys
-    uint32_t sc_nan[SC];              // bit g: s_v of group g is not finite
+    float4 sc[SC][8];                 // s_k, log2 f, 1 / f of 64 or 16 keys
+    uint32_t v_mul[SC][8];            // the power of two of their values, a pair of fp16
+    uint32_t sc_word[SC];             // bit g: s_v of group g is not finite; above: the reference of the values
     uint64_t raw_full[RAW], raw_empty[RAW];
     uint64_t k_full[K16], k_empty[K16], v_full[V16], v_empty[V16];
     uint64_t sc_full[SC], sc_empty[SC];
@@ -109,6 +130,9 @@ ZB_DEVINL void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
         "tcgen05.wait::st.sync.aligned;" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+
+// 2^n of n <= 127 (0 below -126).
+ZB_DEVINL float pow2(int n) { return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 
 // mbar_wait_warp for phases that cannot come round again before this warp arrives: most are
 // there already, and then one vote answers, without a branch that lanes could part at.
@@ -244,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         }
         for (int i = 0; i < SC; ++i) {
             mbar_init(smem_addr(&sm.sc_full[i]), 1);
-            mbar_init(smem_addr(&sm.sc_empty[i]), PAIR ? 8 : 4);
+            mbar_init(smem_addr(&sm.sc_empty[i]), (PAIR ? 8 : 4) + 2);   // softmax warps, and those that convert V
         }
         mbar_init(smem_addr(&sm.other_full), 128);
         mbar_init(smem_addr(&sm.other_empty), 128);
@@ -297,59 +321,29 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             // ==================================================== loader ====
             const int piece_rows = min(B, BN);
             const uint32_t piece_bytes = static_cast<uint32_t>(piece_rows) * HD;
-            const int group_piece = lane * (BN / G) / piece_rows;   // lanes 0..G-1: group of keys -> piece
             Ring<RAW> raw;
-            Ring<SC> sc;
             int issued = 0;
-            bool ok = true, held = false;                      // scales read and not yet put
-            float ks = 0.f, vs = 0.f;
-            auto put_scales = [&]() -> bool {                  // of the tile before
-                if (!wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc)) return false;
-                const bool bad = !(fabsf(vs) <= 3.4e38f);
-                // codes under a zero scale are zeros: any scale does for the product, but the softmax's reference
-                // takes it as well, so a block of zeros counts as one of the smallest values (as 1 it pushed the
-                // other blocks' weights out of fp16).  A scale that is not finite has a path of its own, and 1
-                // keeps -inf * s_k what it is.
-                // Values below 2^-100 * 448 would be lost among anything a sum of weights can hold.
-                const float v = bad ? 1.f : fmaxf(vs, 0x1p-100f);
-                const float lv = log2f(v);
-                if (lane < G) sm.sc[sc.st][lane] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
-                const uint32_t nan = __ballot_sync(0xffffffffu, lane < G && bad);
-                if (lane == 0) sm.sc_nan[sc.st] = nan;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[sc.st]));
-                sc.step();
-                return true;
-            };
+            bool ok = true;
             for (; running && ok; running = items.next(walk)) {
                 for (int t = walk.c0; t < walk.c1; ++t) {
                     const int key0 = t * BN;
                     const int have = (min(walk.len - key0, BN) + piece_rows - 1) / piece_rows;
                     int slot = 0;
                     if (lane < have) slot = slot_of(c, walk.h, (key0 + lane * piece_rows) >> shift, a.status);
-                    if (held && !(ok = put_scales())) break;
                     if (!(ok = wait_warp(smem_addr(&sm.raw_empty[raw.st]), raw.ph ^ 1u, wc))) break;
                     const uint32_t bar = smem_addr(&sm.raw_full[raw.st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(have) * 2 * piece_bytes);
                     __syncwarp();
-                    const long long blk = static_cast<long long>(walk.h) * c.slots + slot;
                     if (lane < have) {
-                        const long long byte = (blk * B + ((key0 + lane * piece_rows) & (B - 1))) * HD;
+                        const long long byte = ((static_cast<long long>(walk.h) * c.slots + slot) * B +
+                                                ((key0 + lane * piece_rows) & (B - 1))) * HD;
                         bulk_load(smem_addr(&sm.raw[raw.st][0][lane * piece_bytes]), c.k + byte, piece_bytes, bar);
                         bulk_load(smem_addr(&sm.raw[raw.st][1][lane * piece_bytes]), c.v + byte, piece_bytes, bar);
                     }
-                    const long long gblk = __shfl_sync(0xffffffffu, blk, group_piece & 31);
-                    ks = vs = 0.f;
-                    if (lane < G && group_piece < have) {
-                        ks = __ldg(c.k_scale + gblk);
-                        vs = __ldg(c.v_scale + gblk);
-                    }
-                    held = true;
                     raw.step();
                     ++issued;
                 }
             }
-            if (ok && held) put_scales();
             // copies in flight still write the ring
             volatile int no_abort = 0;
             const WaitCtx w2{a.status, &no_abort, drain_timeout_ns(a.timeout_ns)};
@@ -425,16 +419,69 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 const WaitCtx w2{a.status, &no_abort, drain_timeout_ns(a.timeout_ns)};
                 mbar_wait(smem_addr(&sm.drain[s]), 0, w2);
             }
-        } else if (lane == 0) {
-            // where the join finds the partial results of the items that begin in this run:
-            // this CTA's place and how many CTAs hold parts, 0 for an item held whole
+        } else {
+            // ==================================================== scales ====
+            constexpr int AHEAD = 32 / G;                      // tiles whose scales the lanes read at once
+            constexpr int KEYS = BN / G;
+            Ring<SC> sc;
+            bool ok = true;
             for (int part = 0; running; running = items.next(walk), ++part) {
-                if (walk.c0 != 0) continue;
-                // the part's first tile and the item's last one, in units of all items
-                const long long first = end - walk.left - (walk.c1 - walk.c0);
-                const long long to = ((first + walk.nc) * ctas - 1) / total;
-                a.item[items.index(walk)] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
-                                                      walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
+                if (walk.c0 == 0 && lane == 0) {
+                    // where the join finds the partial results of an item that begins in this run: this CTA's
+                    // place and how many CTAs hold parts, 0 for an item held whole.  The part's first tile and
+                    // the item's last one, in units of all items:
+                    const long long first = end - walk.left - (walk.c1 - walk.c0);
+                    const long long to = ((first + walk.nc) * ctas - 1) / total;
+                    a.item[items.index(walk)] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
+                                                          walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
+                }
+                if (!ok) continue;                             // the join reads all items all the same
+                int ref = NO_REF;
+                auto fetch = [&](int t, float& ks, float& vs) {
+                    const long long key = static_cast<long long>(t) * BN + lane * KEYS;   // (t + lane / G, group lane % G)
+                    ks = vs = 0.f;
+                    if (t + lane / G < walk.c1 && key < walk.len) {
+                        const long long blk = static_cast<long long>(walk.h) * c.slots + slot_of(c, walk.h, key >> shift, a.status);
+                        ks = __ldg(c.k_scale + blk);
+                        vs = __ldg(c.v_scale + blk);
+                    }
+                };
+                float ks, vs, ks_next = 0.f, vs_next = 0.f;
+                fetch(walk.c0, ks, vs);
+                for (int t0 = walk.c0; t0 < walk.c1 && ok; t0 += AHEAD) {
+                    if (t0 + AHEAD < walk.c1) fetch(t0 + AHEAD, ks_next, vs_next);
+                    const bool bad = !(fabsf(vs) <= 3.4e38f), some = !bad && vs > 0.f;
+                    const uint32_t nan = __ballot_sync(0xffffffffu, bad);
+                    if (some) vs = fminf(vs, 0x1p122f);        // no block of bf16 values has more; 2^e stays a number
+                    const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 126;   // subnormal: -126
+                    const float frac = vs * pow2(-e);
+                    int top = some ? e : NO_REF;               // of the lane's tile
+#pragma unroll
+                    for (int o = 1; o < G; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int n = min(AHEAD, walk.c1 - t0);
+                    for (int i = 0; i < n; ++i) {
+                        const int now = __shfl_sync(0xffffffffu, top, i * G);
+                        if (t0 + i == walk.c0 || now > ref + K_MAX<FMT>) ref = now;
+                        if (!(ok = wait_warp(smem_addr(&sm.sc_empty[sc.st]), sc.ph ^ 1u, wc))) break;
+                        if (lane / G == i) {
+                            const int k = max(e - ref, K_MIN<FMT>), rest = e - ref - k;
+                            // Zeros, and values that 2^-40 of the largest (e4m3: 2^-31) is more than: no values.  A
+                            // scale that is not finite has a path of its own (nan_value).
+                            const bool on = some && rest >= -K_REST;
+                            const float lv = on ? log2f(frac) + static_cast<float>(rest) : 0.f;
+                            // 1 in the place of a key scale of 0 keeps -inf * s_k what it is
+                            sm.sc[sc.st][lane % G] = make_float4(ks == 0.f ? 1.f : ks, lv, ex2(-lv), 0.f);
+                            const uint32_t mul = !on ? 0u : k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : 1u << (k + 24);
+                            sm.v_mul[sc.st][lane % G] = mul << 16 | mul;
+                        }
+                        if (lane == 0) sm.sc_word[sc.st] = ref_word(ref) | (nan >> (i * G) & ((1u << G) - 1u));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[sc.st]));
+                        sc.step();
+                    }
+                    ks = ks_next;
+                    vs = vs_next;
+                }
             }
         }
         __syncwarp();
@@ -443,9 +490,11 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
         // ================================================== converters ====
         const int half = warp & 1, which = (warp >> 1) & 1;   // rows 64 half .., 0: K, 1: V
         const int rot = lane >> 2, piece = lane & 3;          // row within 8, 16-byte piece of it
+        constexpr int HG = G / 2;                             // scales of these rows
         static_assert(K16 == V16, "one ring walk for both");
         Ring<RAW> raw;
         Ring<K16> to;
+        Ring<SC> sc;
         uint64_t* const full = which ? sm.v_full : sm.k_full;
         uint64_t* const empty = which ? sm.v_empty : sm.k_empty;
         uint8_t* const tiles = which ? sm.v16[0] : sm.k16[0];
@@ -462,17 +511,39 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[raw.st]));
                 raw.step();
                 if (!(ok = wait_warp(smem_addr(empty + to.st), to.ph ^ 1u, wc))) break;
+                uint32_t mul[HG];
+                if (which) {
+                    if (!(ok = wait_warp(smem_addr(&sm.sc_full[sc.st]), sc.ph, wc))) break;
+#pragma unroll
+                    for (int i = 0; i < HG; ++i) mul[i] = sm.v_mul[sc.st][half * HG + i];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[sc.st]));
+                    sc.step();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < HG; ++i) mul[i] = 0x3C003C00u;
+                }
                 uint8_t* dst = tiles + to.st * TILE_BYTES;
                 // values behind the last token must be finite: what the ring holds there is anything
                 const int valid = which ? min(walk.len - t * BN, BN) : BN;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int row = half * 64 + i * 8 + rot;
+                    const uint32_t by = mul[i / (8 / HG)];
                     uint32_t o[8];
-                    unpack4<FMT>(w[i].x, o[0], o[1]);
-                    unpack4<FMT>(w[i].y, o[2], o[3]);
-                    unpack4<FMT>(w[i].z, o[4], o[5]);
-                    unpack4<FMT>(w[i].w, o[6], o[7]);
+                    if (FMT == ZB_KV8_INT8) {                  // the factor costs nothing here
+                        unpack4_int8(w[i].x, by, o[0], o[1]);
+                        unpack4_int8(w[i].y, by, o[2], o[3]);
+                        unpack4_int8(w[i].z, by, o[4], o[5]);
+                        unpack4_int8(w[i].w, by, o[6], o[7]);
+                    } else {
+                        unpack4<FMT>(w[i].x, o[0], o[1]);
+                        unpack4<FMT>(w[i].y, o[2], o[3]);
+                        unpack4<FMT>(w[i].z, o[4], o[5]);
+                        unpack4<FMT>(w[i].w, o[6], o[7]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], by);
+                    }
                     if (row >= valid) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) o[k] = 0u;
@@ -506,6 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             const bool live = r_head < a.rows;
             const long long out_row = static_cast<long long>(walk.h) * a.rows + r_head;
             float m = -INFINITY, l = 0.f;
+            uint32_t last = ref_word(NO_REF);                  // the reference of the values so far
             bool nan_value = false;
             if (j0 < n) {
                 // Q: the row's largest to [2^14, 2^15), as in kv8_attn.cu.  All of the slot's earlier
@@ -539,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     mbar_arrive(smem_addr(&sm.q_full[s]));
                 }
                 const int lim = a.causal ? walk.len - a.n_q + 1 + r_head % a.n_q : walk.len;
-                // weight sums of this part's tiles, in order (SPLIT: every second tile)
+                // weight sums of this part's tiles, in order (where slots share rows: every second tile)
                 const int per_tile = G / per_sum;
                 int gsum_left = a.groups - (walk.c0 + j0) * per_tile;
                 float* gsum = a.gsum + (static_cast<long long>(walk.h) * a.groups + static_cast<long long>(walk.c0 + j0) * per_tile) * a.rows + r_head;
@@ -551,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     const int seen = max(min(lim - (walk.c0 + j) * BN, BN), 0);
                     float alpha = 1.f, nm = 0.f, weight = 0.f;
                     bool raise = false;
+                    int grown = 0;                             // less what the values' reference grew by
                     // A tile is read in halves, the first half twice: for the maximum, and again for its
                     // exponentials after the second half's.  Held whole, its 128 values left the compiler so
                     // few registers that it moved each about once more than needed.  Tiles that every row
@@ -581,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                             float mx = -INFINITY;
 #pragma unroll
                             for (int q = 0; q < HG; ++q) {
-                                const float2 w = *reinterpret_cast<const float2*>(&sm.sc[sc][h * HG + q]);
+                                const float ks = sm.sc[sc][h * HG + q].x;
                                 float v = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < COLS; k += 16) { // a tree of 3-input maxima
@@ -590,7 +663,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                                     for (int e = 3; e < 15; e += 2) u = fmax3(u, x[COLS * q + k + e], x[COLS * q + k + e + 1]);
                                     v = fmax3(v, u, x[COLS * q + k + 15]);
                                 }
-                                mx = fmaxf(mx, fmaf(v, factor(w.x, h * HG + q), w.y));
+                                mx = fmaxf(mx, v * factor(ks, h * HG + q));
                             }
                             return mx;
                         };
@@ -624,8 +697,11 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         float mx = maximum(0, x);
                         load(1, x);
                         mx = fmaxf(mx, maximum(1, x));
-                        if (const uint32_t bad = sm.sc_nan[sc]; bad)
-                            nan_value |= (bad & ((1u << ((seen + COLS - 1) / COLS)) - 1u)) != 0;
+                        if (const uint32_t word = sm.sc_word[sc]; word != last) {
+                            nan_value |= (word & 0xFFu & ((1u << ((seen + COLS - 1) / COLS)) - 1u)) != 0;
+                            if (j > j0) grown = word_ref(last) - word_ref(word);
+                            last = word & ~0xFFu;
+                        }
                         raise = mx > m + RAISE || (m == -INFINITY && mx > m);
                         if (raise) {
                             alpha = m == -INFINITY ? 0.f : ex2(m - mx);
@@ -644,8 +720,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         return true;
                     };
                     if (!(ok = __any_sync(0xffffffffu, seen < BN) ? step(std::true_type{}) : step(std::false_type{}))) break;
-                    if (__any_sync(0xffffffffu, raise && j > j0)) {
-                        const float al = raise && j > j0 ? alpha : 1.f;
+                    if (__any_sync(0xffffffffu, (raise && j > j0) || grown != 0)) {
+                        const float al = (raise && j > j0 ? alpha : 1.f) * pow2(grown);
                         uint32_t ro[HD];
                         tmem_load(tm_o, ro);
 #pragma unroll
@@ -680,12 +756,15 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < HD; ++e) o[e] = 0.f;
             }
-            if (nan_value) {
+            {
+                // the row's outputs as they are, without the references: no part's depend on another's
+                const float inv = l == 0.f ? 0.f : 1.f / l;    // no key: zeros; NaN stays
+                const float size = pow2(word_ref(last));
 #pragma unroll
-                for (int e = 0; e < HD; ++e) o[e] = __uint_as_float(0x7FC00000u);
+                for (int e = 0; e < HD; ++e) o[e] = nan_value ? __uint_as_float(0x7FC00000u) : o[e] * inv * size;
             }
             if (!PAIR) {
-                // the slots hold the same rows: slot 1 hands its sums to slot 0
+                // the slots hold the same rows: slot 1 hands its outputs to slot 0
                 if (s == 1) {
                     if (!(ok = wait_warp(smem_addr(&sm.other_empty), (part & 1) ^ 1, wc))) break;
 #pragma unroll
@@ -698,9 +777,10 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                 if (!(ok = wait_warp(smem_addr(&sm.other_full), part & 1, wc))) break;
                 const float2 ml = sm.other_ml[row];
                 const float M = fmaxf(m, ml.x);
-                const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                const float l0 = m == -INFINITY ? l : l * ex2(m - M), l1 = ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - M);
                 m = M;
-                l = l * f0 + ml.y * f1;
+                l = l0 + l1;
+                const float inv = l == 0.f ? 0.f : 1.f / l, f0 = l0 * inv, f1 = l1 * inv;
 #pragma unroll
                 for (int i = 0; i < HD / 4; ++i) {
                     const float4 w = sm.other[i][row];
@@ -713,14 +793,11 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             }
             if (!live) continue;
             if (walk.c0 == 0 && walk.c1 == walk.nc) {          // the whole item: the outputs themselves
-                const float inv = l == 0.f ? 0.f : 1.f / l;    // no key: zeros; NaN stays
                 uint4* out = reinterpret_cast<uint4*>(a.O + out_row * HD);
 #pragma unroll
                 for (int i = 0; i < HD / 8; ++i)
-                    out[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                        pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                        pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                        pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    out[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                        pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
                 const float total2 = l == 0.f ? -INFINITY : m - SHIFT + log2f(l);
                 if (a.lse) a.lse[out_row] = total2 * LN2;
                 if (a.lse2) a.lse2[out_row] = total2;
@@ -741,9 +818,10 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
     }
 }
 
-// The parts of items that several CTAs hold, added up; rows of items without a tile
-// become zeros and -inf.  Grid: (row tiles, 8): 16 rows a CTA, 16 threads a row.  A
-// row's thread reads one part's maximum and sum in sixteen and 4 features of all.
+// The parts of items that several CTAs hold, each the outputs over its own keys, added
+// up by their shares of the softmax sum; rows of items without a tile become zeros and
+// -inf.  Grid: (row tiles, 8): 16 rows a CTA, 16 threads a row.  A row's thread reads
+// one part's maximum and sum in sixteen and 4 features of all.
 template <bool PAIR>
 __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
     const int per_item = PAIR ? 2 : 1, row_tiles = a.tiles * per_item;
@@ -766,16 +844,17 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
     for (int i = q; i < it.y; i += 16) M = fmaxf(M, a.part_ml[at(i)].x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+    auto share = [&](int i) {                        // of the softmax sum, over 2^M
+        const float2 ml = a.part_ml[at(i)];
+        return ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - M);
+    };
+    for (int i = q; i < it.y; i += 16) L += share(i);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) L += __shfl_xor_sync(half, L, o);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < it.y; i0 += 16) {
-        float f = 0.f, l = 0.f;
-        if (i0 + q < it.y) {
-            const float2 ml = a.part_ml[at(i0 + q)];
-            if (ml.y != 0.f) {
-                f = ex2(ml.x - M);
-                l = ml.y * f;
-            }
-        }
+        const float f = i0 + q < it.y ? share(i0 + q) * inv : 0.f;
         const int n = min(16, it.y - i0);
         for (int i1 = 0; i1 < n; i1 += 4) {
             float4 v[4];
@@ -784,10 +863,8 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
                 v[k] = i1 + k < n ? reinterpret_cast<const float4*>(a.part_o + at(i0 + i1 + k) * HD)[q]
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; ++k) {            // lanes past the last part hold zeros
                 const float fk = __shfl_sync(half, f, (i1 + k) & 15, 16);
-                L += __shfl_sync(half, l, (i1 + k) & 15, 16);   // lanes past the last part hold zeros
-                if (fk == 0.f) continue;
                 sum.x = fmaf(v[k].x, fk, sum.x);
                 sum.y = fmaf(v[k].y, fk, sum.y);
                 sum.z = fmaf(v[k].z, fk, sum.z);
@@ -795,11 +872,10 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
             }
         }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
     const float total2 = L == 0.f ? -INFINITY : M - SHIFT + log2f(L);
     const long long row = static_cast<long long>(h) * a.rows + r_head;
     reinterpret_cast<uint2*>(a.O + row * HD)[q] =
-        make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
     if (q == 0) {
         if (a.lse) a.lse[row] = total2 * LN2;
         if (a.lse2) a.lse2[row] = total2;

@@ -103,3 +103,131 @@ def test_blocks_of_zero_values(fmt, block, G, n_q, causal):
         c, ora, lens = _made(zb, K, V, block, fmt, 24)
         _check(zb, c, ora, lens, queries(G, n_q), G, causal, 0.125)
 
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("block", [16, 128])
+@pytest.mark.parametrize("G,n_q,causal", ROWS)
+def test_a_block_of_large_values_under_most_of_the_weight(fmt, block, G, n_q, causal):
+    # its other features are zeros: there the outputs are the many keys' of hardly any weight
+    import linear_hybrid_attention_b200 as zb
+    n = 6000
+    for times, first in ((2.0 ** 10, 0), (2.0 ** 14, 0), (2.0 ** 14, 4096)):
+        K, queries = _loaded(2, n, 10.0, 31, at=first + 3)
+        V = _rand((2, n, 64), 33).float().cpu()
+        V[:, first:first + block] *= times
+        V[:, first:first + block, 32:] = 0
+        c, ora, lens = _made(zb, K, V, block, fmt, 34)
+        _check(zb, c, ora, lens, queries(G, n_q), G, causal, 0.125)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n_q,causal", ROWS)
+def test_scales_far_apart(fmt, G, n_q, causal):
+    # scales from 2^-40 to 2^100, up and down along the keys: sums, lse and weights do not depend on them; a value
+    # may be lost that is 2^-31 of the head's largest
+    import linear_hybrid_attention_b200 as zb
+    n, block = 2000, 64
+    K = _rand((3, n, 64), 41, 0.3).float().cpu()
+    V = _rand((3, n, 64), 42).float().cpu()
+    step = torch.arange(n) // 256
+    V[0] *= torch.exp2(-40 + 20.0 * step)[:, None]
+    V[1] *= torch.exp2(100 - 20.0 * step)[:, None]
+    V[2] *= torch.exp2(torch.where(step % 2 == 0, 100.0, -40.0))[:, None]
+    c, ora, lens = _made(zb, K, V, block, fmt, 43)
+    _check(zb, c, ora, lens, _rand((3 * G, n_q, 64), 44, 0.3), G, causal, 0.125, rel_v=2.0 ** -31)
+
+
+@pytest.mark.parametrize("G,n_q,causal", MANY)
+def test_values_at_both_ends_of_their_type(G, n_q, causal):
+    # bf16 goes to 3.4e38; values of 2^-110 and 30,000 keys of nearly equal weight
+    import linear_hybrid_attention_b200 as zb
+    K, V = _rand((1, 700, 64), 51, 0.3).float().cpu(), torch.randn((1, 700, 64), generator=torch.Generator().manual_seed(52))
+    c, ora, lens = _made(zb, K, V.clamp(-3, 3) * 2.0 ** 126, 64, "int8", 53)
+    _check(zb, c, ora, lens, _rand((G, n_q, 64), 54, 0.3), G, causal, 0.125)
+    n = 30000
+    K = torch.randn((1, n, 64), generator=torch.Generator().manual_seed(55)) * 0.1
+    V = torch.rand((1, n, 64), generator=torch.Generator().manual_seed(56)) * 2.0 ** -110
+    c, ora, lens = _made(zb, K, V, 64, "int8", 57)
+    _check(zb, c, ora, lens, _rand((G, n_q, 64), 58, 0.3), G, causal, 0.125)
+
+
+# ------------------------------------------------------------ logits, queries ----
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("G,n_q,causal", ROWS)
+def test_logits_that_keep_rising(block, G, n_q, causal):
+    # the maximum moves with every tile, by little and by much; then back down
+    import linear_hybrid_attention_b200 as zb
+    n, q, scale = 2500, 4.0, 0.125
+    K = _rand((2, n, 64), 61, 0.3).float().cpu()
+    ramp = torch.arange(n).float() / n
+    K[0, :, 0] = ramp * 60.0 / (q * scale)
+    K[1, :, 0] = torch.where(ramp < 0.5, ramp * 200.0, 100.0 - 30.0 * ramp) / (q * scale)
+    c, ora, lens = _made(zb, K, _rand((2, n, 64), 62).float(), block, "int8", 63)
+    Q = _rand((2 * G, n_q, 64), 64, 0.3)
+    Q[..., 0] = q
+    _check(zb, c, ora, lens, Q, G, causal, scale)
+
+
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("G,n_q,causal", MANY)
+def test_query_sizes_of_many_rows(block, G, n_q, causal):
+    # queries far outside fp16's range, tiny ones, zeros, and all of them in one call
+    import linear_hybrid_attention_b200 as zb
+    K, V = _rand((1, 700, 64), 71, 0.3).float(), _rand((1, 700, 64), 72).float()
+    c, ora, lens = _made(zb, K, V, block, "e4m3", 73)
+    Q = _rand((G, n_q, 64), 74, 0.3)
+    _check(zb, c, ora, lens, Q * 2.0 ** 40, G, causal, 2.0 ** -43)
+    _check(zb, c, ora, lens, Q * 2.0 ** -60, G, causal, 2.0 ** 57)
+    Q = Q * torch.exp2(-20.0 * (torch.arange(n_q, device="cuda") % 4))[:, None].bfloat16()
+    Q[:, ::5] = 0
+    _check(zb, c, ora, lens, Q, G, causal, 0.125)
+
+
+@pytest.mark.parametrize("block", [16, 64, 128])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("G,n_q", [(1, 24), (1, 40), (2, 60), (1, 150), (2, 140)])
+def test_not_finite_blocks_spoil_the_rows_that_see_them(block, which, G, n_q):
+    import linear_hybrid_attention_b200 as zb
+    n = 500
+    K, V = _rand((2, n, 64), 81, 0.3).float().cpu(), _rand((2, n, 64), 82).float().cpu()
+    bad = (n - n_q // 2) // block                        # begins within the causal rows' ends, or before
+    first = bad * block
+    (K if which == "k" else V)[1, first, 5] = float("inf") if block == 16 else float("nan")
+    c, ora, lens = _made(zb, K, V, block, "int8", 83)
+    Q = _rand((2 * G, n_q, 64), 84, 0.3)
+    O, lse = zb.zb_kv8_attn(Q, c, lens, causal=True, scale=0.125, want_lse=True)
+    sync_ok()
+    sees = torch.arange(n_q) + n - n_q >= first          # of the rows of head 1
+    O, lse = O.reshape(2, G, n_q, 64).cpu(), lse.reshape(2, G, n_q).cpu()
+    assert torch.isfinite(O[0]).all() and torch.isfinite(lse[0]).all()
+    assert torch.isnan(O[1][:, sees]).all()
+    assert torch.isnan(lse[1][:, sees]).all() if which == "k" else torch.isfinite(lse[1]).all()
+    # the others are what they are without that block's tokens
+    if (~sees).any():
+        ora[1].k, ora[1].v = np.nan_to_num(ora[1].k, posinf=0), np.nan_to_num(ora[1].v, posinf=0)
+        rows = np.broadcast_to((~sees).numpy(), (G, n_q))
+        Kr, Vr = ora[1].values()[:2]
+        q64 = host(Q).reshape(2, G, n_q, 64)[1]
+        refO = oracle.cache_attention(q64, Kr, Vr, 0.125, True, block)[0]
+        absO = oracle.cache_attention(q64, Kr, np.abs(Vr), 0.125, True, block)[0]
+        d = 64 * 2.0 ** -23 * 0.125 * np.max(np.abs(q64) @ np.abs(Kr).T, -1)[..., None]
+        bound = 2.0 ** -8 * np.abs(refO) + (2 * d + 2.0 ** -11 + 2.0 ** -18) * absO + 2.0 ** -31 * np.abs(Vr).sum(0)
+        assert np.all((np.abs(host(O[1]) - refO) <= bound)[rows])
+
+
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("G,n_q,causal", ROWS)
+def test_queries_that_are_not_finite_spoil_their_own_rows(block, G, n_q, causal):
+    import linear_hybrid_attention_b200 as zb
+    c, ora, lens = _made(zb, _rand((1, 700, 64), 91, 0.3).float(), _rand((1, 700, 64), 92).float(), block, "int8", 93)
+    Q = _rand((G, n_q, 64), 94, 0.3)
+    bad = torch.zeros((G, n_q), dtype=torch.bool)
+    bad[0, 3] = bad[-1, n_q - 1] = True
+    Q[0, 3, 9], Q[-1, n_q - 1, 63] = float("inf"), float("nan")
+    got, lse = zb.zb_kv8_attn(Q, c, lens, causal=causal, want_lse=True)
+    assert torch.isnan(got[bad.cuda()]).all() and torch.isnan(lse[bad.cuda()]).all()
+    clean = Q.clone()
+    clean[0, 3, 9] = clean[-1, n_q - 1, 63] = 0
+    want, wl = zb.zb_kv8_attn(clean, c, lens, causal=causal, want_lse=True)
+    assert torch.equal(got[~bad.cuda()], want[~bad.cuda()]) and torch.equal(lse[~bad.cuda()], wl[~bad.cuda()])
+    sync_ok()
