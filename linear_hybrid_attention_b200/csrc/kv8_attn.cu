@@ -42,6 +42,11 @@ constexpr int WARPS = 12;
 constexpr int STAGES = 2;
 constexpr int TILE = 16;                         // most query rows of an item (8 if there are no more)
 constexpr uint32_t HALF_STAGE = CHUNK * HD;      // 4 KB of codes
+// Sums of weights (up to 2^P_SHIFT a key) times values pass fp32 where values near the end
+// of bf16's range meet many keys.  From the first value scale above VAST on, a part's sums
+// are held times VAST_MUL (what that takes off values below 2^-62 is nothing beside those),
+// and all parts leave theirs times O_UNIT: room for 2^18 keys of the largest weight and value.
+constexpr float VAST = 0x1p64f, VAST_MUL = 0x1p-64f, O_UNIT = 0x1p-32f;
 
 // A warp's part of an item that others hold parts of too (item -1: none).  Entry 2 w
 // is the part that warp w's run starts with, in its row of part_o; entry 2 w + 1 the
@@ -294,6 +299,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         }
         float o[NT][4][4];                           // features 8 g + 2 j + (0, 0, 1, 1), rows 8 n + 2 c4 + (0, 1, 0, 1)
         float m[NT][2], l[NT][2];
+        float v_mul = 1.f;                           // of the sums: VAST_MUL once a value is vast
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -420,16 +426,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                     pb[n][t][1] = transpose8(pack_f16x2(x[n][t][2], x[n][t][3]));
                 }
             }
-            bool moved = false;
+            bool moved = vsl * v_mul > VAST;
 #pragma unroll
             for (int n = 0; n < NT; ++n) moved |= corr[n][0] != 1.f || corr[n][1] != 1.f;
             if (__any_sync(0xffffffffu, moved)) {    // rare once the maxima settle
+                float down = 1.f;
+                if (__any_sync(0xffffffffu, vsl * v_mul > VAST)) v_mul = down = VAST_MUL;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][j][e] *= corr[n][e & 1];
+                        for (int e = 0; e < 4; ++e) o[n][j][e] *= corr[n][e & 1] * down;
                     }
                 }
             }
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                         }
                     }
                 }
-                const float vs = __shfl_sync(0xffffffffu, vsl, p);
+                const float vs = __shfl_sync(0xffffffffu, vsl, p) * v_mul;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     // a row that sees nothing of the piece takes nothing of it, whatever its scale is
@@ -491,6 +499,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
         const int e2 = 2 * warp + (last ? 1 : 0);
         float* dst = last ? reinterpret_cast<float*>(&ring[0][0][0])
                           : a.part_o + (a.runs + static_cast<long long>(blockIdx.x) * WARPS + warp) * TR * HD;
+        const float unit = v_mul == 1.f ? O_UNIT : O_UNIT / VAST_MUL;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][j][e] *= unit;
+            }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 if (whole) {
                     if (r < live_rows) {
                         const long long row = static_cast<long long>(cur.h) * a.rows + row0 + r;
-                        const float inv = L == 0.f ? 0.f : 1.f / L;      // no key: zeros; NaN stays
+                        const float inv = L == 0.f ? 0.f : 1.f / O_UNIT / L;   // no key: zeros; NaN stays
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(o[n][j][i] * inv, o[n][j][2 + i] * inv);
@@ -574,7 +591,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
                 }
                 if (q == 0) a.part_ml[run * TR + r] = make_float2(M, L);
                 if (whole) {
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    const float inv = L == 0.f ? 0.f : 1.f / O_UNIT / L;
                     const long long row = static_cast<long long>(h) * a.rows + row0 + r;
                     reinterpret_cast<uint2*>(a.O + row * HD)[q] =
                         make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
@@ -694,7 +711,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
             const float t = L == 0.f ? -INFINITY : M - P_SHIFT + log2f(L);
             if (q == 0) lse2[row] = t;
             if (part == 0 && it.y > 1) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const float inv = L == 0.f ? 0.f : 1.f / O_UNIT / L;
                 const long long out = static_cast<long long>(h) * a.rows + row;
                 reinterpret_cast<uint2*>(a.O + out * HD)[q] =
                     make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
