@@ -34,7 +34,9 @@ ZB_DEVINL float exact_round(float x, float s, float t) {
     return k + ((r > 0.f || (r == 0.f && odd)) ? 1.f : 0.f);
 }
 
-constexpr float TINY_SCALE = 0x1p-120f;   // 1 / s overflows below about 2^-128
+// From here on 1 / s is a number, half a step of any code (2^-10 s at least) is a normal one,
+// and so the sign that exact_round looks at is right.
+constexpr float TINY_SCALE = 0x1p-110f;
 
 // Eight codes of x for a scale of at least TINY_SCALE.  Adding 1.5 * 2^23 rounds a
 // quotient to a whole number (ties to even) whose low byte is the code: half the
@@ -102,15 +104,17 @@ ZB_DEVINL uint2 codes_e4m3(const float* x, float s, float inv) {
 template <int FMT>
 ZB_DEVINL uint2 codes8(const float* x, float s, float inv) {
     if (s >= TINY_SCALE) return FMT == ZB_KV8_INT8 ? codes_int8(x, s, inv) : codes_e4m3(x, s, inv);
-    // a scale that is subnormal or nearly so: divide, and hold the result to the format
+    // A tiny scale: both numbers times 2^64, which is exact.  A subnormal one may be rounded so far
+    // that quotients pass the format's largest value: held to it.
+    const float big = s * 0x1p64f;
     uint32_t w[2] = {0u, 0u};
     for (int i = 0; i < 8; ++i) {
-        const float t = x[i] / s;
+        const float y = x[i] * 0x1p64f, t = y / big;
         uint32_t c;
         if (FMT == ZB_KV8_INT8)
-            c = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(exact_round(x[i], s, t), -127.f), 127.f))) & 0xFFu;
+            c = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(exact_round(y, big, t), -127.f), 127.f))) & 0xFFu;
         else
-            c = pack_e4m3x2(t != 0.f ? value_e4m3(x[i], s, t) : t, 0.f) & 0xFFu;
+            c = pack_e4m3x2(t != 0.f ? value_e4m3(y, big, t) : t, 0.f) & 0xFFu;
         w[i >> 2] |= c << (8 * (i & 3));
     }
     return make_uint2(w[0], w[1]);

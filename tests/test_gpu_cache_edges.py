@@ -231,3 +231,33 @@ def test_queries_that_are_not_finite_spoil_their_own_rows(block, G, n_q, causal)
     want, wl = zb.zb_kv8_attn(clean, c, lens, causal=causal, want_lse=True)
     assert torch.equal(got[~bad.cuda()], want[~bad.cuda()]) and torch.equal(lse[~bad.cuda()], wl[~bad.cuda()])
     sync_ok()
+
+
+# --------------------------------------------------------------- exact rounding ----
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("low,high", [(1.0, 2.0), (2.0 ** -104, 2.0 ** -98), (2.0 ** -122, 2.0 ** -104), (2.0 ** -131, 2.0 ** -122)])
+def test_ties_of_every_scale(fmt, low, high):
+    # values within bf16's rounding of a tie between two codes, for scales with few and many bits, tiny ones among them
+    import linear_hybrid_attention_b200 as zb
+    rng = np.random.default_rng(101)
+    grid = np.arange(128.0) if fmt == "int8" else oracle.E4M3_VALUES
+    x = np.zeros((64, 64, 64))
+    for h in range(64):
+        top = float(torch.tensor(np.exp(rng.uniform(np.log(low), np.log(high)))).bfloat16())
+        s = float(np.float32(top / grid[-1]))
+        k = rng.integers(0, len(grid) - 2, (64, 64))
+        x[h] = np.where(rng.random((64, 64)) < 0.5, 1, -1) * (grid[k] + grid[k + 1]) / 2 * s
+        x[h, 0, 0] = top
+    X = torch.from_numpy(x).bfloat16()
+    X = torch.where(X.abs() > X[:, :1, :1], X[:, :1, :1], X).cuda()
+    c = zb.KV8Cache.empty(64, 64, 64, fmt)
+    zb.zb_kv8_append(c, X, X, _ints([0] * 64))
+    sync_ok()
+    codes = c.k[:, 0].double().cpu().numpy()
+    for h in range(64):
+        q, s = oracle.quantise_block(host(X[h]), fmt)
+        assert float(c.k_scale[h, 0].double()) == s
+        np.testing.assert_array_equal(codes[h], q)
+    K, _ = zb.zb_kv8_read(c, _ints([64] * 64), 64)
+    want = torch.from_numpy(np.asarray(codes * c.k_scale[:, 0].double().cpu().numpy()[:, None, None], np.float32))
+    assert torch.equal(K.cpu(), want.bfloat16())
