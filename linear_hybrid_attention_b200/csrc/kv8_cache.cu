@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(A_THREADS, 4) append_kernel(const AppendArgs a
     const zb_kv8& c = a.c;
     const int B = c.block, shift = 31 - __clz(B);   // B is a power of two
     const long long cap = static_cast<long long>(c.slots) * B;
-    const long long len = __ldg(a.lens + h);
+    const long long len = __ldca(a.lens + h);       // (lens_out may be lens)
     if (len < 0 || len + a.n > cap) {          // does not fit: the head stays as it is
         if (unit == 0 && threadIdx.x == 0) {
             flag_status(a.status, ZB_ERR_INDEX);
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(const EvictArgs a) {
     const int32_t* table = a.table + row;
     int32_t* out = a.table_out + row;
     int32_t* kept = a.kept ? a.kept + static_cast<long long>(h) * a.budget : nullptr;
-    const long long len = head_len(a.lens, h, static_cast<long long>(a.slots) * a.block);
+    const long long had = __ldca(a.lens + h);       // (lens_out may be lens)
+    const long long len = min(max(had, 0ll), static_cast<long long>(a.slots) * a.block);
     const int nb = static_cast<int>((len + a.block - 1) / a.block);
     if (nb <= a.budget) {
         for (int b = tid; b < a.slots; b += THREADS) out[b] = table[b];

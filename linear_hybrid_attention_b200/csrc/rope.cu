@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) row_kernel(const Args a) {
         // the next ROWS rows are on their way while these are worked on
         uint4 xv[ROWS][2], gv[BACK ? ROWS : 1][2];
         auto load = [&](int k) {
-            xv[k][0] = __ldg(x + c0);
-            xv[k][1] = __ldg(x + c1);
+            // forward the output may be the input: not the path for memory that no one writes
+            xv[k][0] = BACK ? __ldg(x + c0) : __ldca(x + c0);
+            xv[k][1] = BACK ? __ldg(x + c1) : __ldca(x + c1);
             x += xh;
             if (BACK) {
                 gv[k][0] = live ? __ldg(g + c0) : make_uint4(0, 0, 0, 0);

@@ -1,5 +1,6 @@
 """The 8-bit cache's attention where values, logits and scales are uneven, for every kernel that serves it: few query
-rows of a cache head (up to 32) and many (items of 128 rows, and of 256).
+rows of a cache head (up to 32) and many (items of 128 rows, and of 256); exact rounding of every scale; calls that
+write where they read.
 
 Tolerances.  Logits, sums, log-sum-exp and weights as in test_gpu_cache.py, whose d, 2^-11 and 2^-18 these are.  A
 softmax weight enters the product as fp16.  Its largest of a row is there at 2^6 at least, so what is below fp16's
@@ -261,3 +262,38 @@ def test_ties_of_every_scale(fmt, low, high):
     K, _ = zb.zb_kv8_read(c, _ints([64] * 64), 64)
     want = torch.from_numpy(np.asarray(codes * c.k_scale[:, 0].double().cpu().numpy()[:, None, None], np.float32))
     assert torch.equal(K.cpu(), want.bfloat16())
+
+
+# ------------------------------------------------------ calls that write where they read ----
+@pytest.mark.parametrize("N", [1, 63, 65, 700])
+@pytest.mark.parametrize("H", [1, 3, 16])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotation_in_place(N, H, layout):
+    # idle lanes, rows of several groups of tokens, many times over: the same bits as into memory of its own
+    import linear_hybrid_attention_b200 as zb
+    X = _rand((2, H, N, 64), 111)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")[None, None] + 100_000
+    turns = zb.zb_rope_frequencies(64).turns.cuda()
+    want = zb.zb_rope(X, pos, turns, layout=layout)
+    for _ in range(20):
+        Y = X.clone()
+        zb.zb_rope(Y, pos, turns, layout=layout, out=Y)
+        assert torch.equal(Y, want)
+    sync_ok()
+
+
+def test_lengths_advanced_in_place():
+    # by an append and an eviction, of more heads than run at once
+    import linear_hybrid_attention_b200 as zb
+    H, block = 3000, 16
+    X = _rand((H, 5, 64), 112)
+    lens = (torch.arange(H, dtype=torch.int32, device="cuda") * 7) % 200
+    a, b = (zb.KV8Cache.empty(H, 256, block) for _ in range(2))
+    inplace = lens.clone()
+    want = zb.zb_kv8_append(a, X, X, lens)
+    zb.zb_kv8_append(b, X, X, inplace, lens_out=inplace)
+    assert torch.equal(inplace, want) and torch.equal(want, lens + 5) and torch.equal(a.k, b.k)
+    _, less, _ = zb.zb_kv8_evict(a.table, a.mass, want, block, 3)
+    zb.zb_kv8_evict(a.table, a.mass, inplace, block, 3, lens_out=inplace)
+    assert torch.equal(inplace, less)
+    sync_ok()
