@@ -225,7 +225,10 @@ class CachedAttention:
             self._kept = torch.empty((batch * kv_heads, budget), dtype=torch.int32, device=dev)
 
     def step(self, Q, K, V, pos=None, causal: bool = True) -> torch.Tensor:
-        """O [B, heads, n, 64] of the new tokens; they are in the cache afterwards."""
+        """O [B, heads, n, 64] of the new tokens; they are in the cache afterwards.
+
+        A head without room for them (lens + n above the cache's capacity) stays as it is and its queries get
+        zeros and add no weight; ``lens`` does not grow there, and the device status says ZB_ERR_INDEX."""
         B, H, G = self.batch, self.heads, self.kv_heads
         n = Q.shape[2] if isinstance(Q, torch.Tensor) and Q.dim() == 4 else -1
         for t, shape, name in ((Q, (B, H, n, HEAD_DIM), "Q"), (K, (B, G, n, HEAD_DIM), "K"), (V, (B, G, n, HEAD_DIM), "V")):
@@ -234,8 +237,10 @@ class CachedAttention:
         if self.turns is not None or self.how["norm"] != "none":
             Q, K = zb_qk_norm_rope(Q, K, pos, self.turns, **self.how)
         K, V, Q = (t.reshape(-1, n, HEAD_DIM).contiguous() for t in (K, V, Q))
+        room = self.lens <= self.cache.capacity - n
         zb_kv8_append(self.cache, K, V, self.lens, lens_out=self.lens)
-        O = zb_kv8_attn(Q, self.cache, self.lens, causal=causal, scale=self.scale, add_mass=self.budget is not None)
+        O = zb_kv8_attn(Q, self.cache, self.lens * room, causal=causal, scale=self.scale,
+                        add_mass=self.budget is not None)
         return O.view(B, H, n, HEAD_DIM)
 
     def evict(self) -> torch.Tensor:

@@ -297,3 +297,38 @@ def test_lengths_advanced_in_place():
     zb.zb_kv8_evict(a.table, a.mass, inplace, block, 3, lens_out=inplace)
     assert torch.equal(inplace, less)
     sync_ok()
+
+
+# ------------------------------------------------------------- the layer's refusals ----
+def test_layer_with_full_heads():
+    """A head without room: zeros for its queries, no weight added, its cache as it was; the others go on."""
+    import linear_hybrid_attention_b200 as zb
+    B, H, G, block = 2, 4, 2, 16
+    make = lambda: zb.CachedAttention(B, H, G, 4 * block, block, "int8", norm="rms", budget=4)
+    one, all_ = make(), make()
+    X = _rand((B, H + 2 * G, 60, 64), 121, 0.3)
+    split = lambda x: (x[:, :H], x[:, H:H + G], x[:, H + G:])
+    for layer in (one, all_):
+        layer.step(*split(X[:, :, :50]))
+    one.lens[1] = one.lens[2] = 60                       # of sequence 0, head 1 and of sequence 1, head 0: 60 + 10 > 64
+    k, mass, tail = one.cache.k.clone(), one.cache.mass.clone(), one.cache.k_tail.clone()
+    O = one.step(*split(X[:, :, 50:]))
+    want = all_.step(*split(X[:, :, 50:]))
+    with pytest.raises(zb.ZbError, match="INDEX"):
+        sync_ok()
+    assert one.lens.tolist() == [60, 60, 60, 60]
+    O, want = (t.reshape(B * G, -1, 10, 64) for t in (O, want))
+    for h in range(B * G):
+        if h in (1, 2):
+            assert not O[h].any() and torch.equal(one.cache.k[h], k[h]) and torch.equal(one.cache.k_tail[h], tail[h])
+            assert torch.equal(one.cache.mass[h], mass[h])
+        else:
+            # (runs of other lengths: each within half a bf16 step and 2^-11 + 2^-18 of the values; d <= 2^-14)
+            near = 2.0 ** -7 * want[h].float().abs() + 2.0 ** -9 * X.float().abs().max()
+            assert ((O[h].float() - want[h].float()).abs() <= near).all() and O[h].any()
+            torch.testing.assert_close(one.cache.mass[h], all_.cache.mass[h], rtol=2.0 ** -12, atol=0)
+    # all heads full: nothing changes
+    lens = one.lens.clone()
+    assert not one.step(*split(X[:, :, :10])).any() and torch.equal(one.lens, lens)
+    with pytest.raises(zb.ZbError, match="INDEX"):
+        sync_ok()
