@@ -209,6 +209,8 @@ class CachedAttention:
                  recent: int = 2, scale: Optional[float] = None, device="cuda"):
         if kv_heads < 1 or heads % kv_heads:
             raise ValueError(f"heads must be a multiple of kv_heads, got {heads} and {kv_heads}")
+        if scale is not None and not 0.0 < scale <= 3.4e38:
+            raise ValueError(f"scale must be a positive number, got {scale}")
         self.batch, self.heads, self.kv_heads = batch, heads, kv_heads
         self.cache = KV8Cache.empty(batch * kv_heads, capacity, block, format, mass=budget is not None, device=device)
         dev = self.cache.device
@@ -234,6 +236,11 @@ class CachedAttention:
         for t, shape, name in ((Q, (B, H, n, HEAD_DIM), "Q"), (K, (B, G, n, HEAD_DIM), "K"), (V, (B, G, n, HEAD_DIM), "V")):
             if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
                 raise ValueError(f"{name} must be {shape}, got {tuple(getattr(t, 'shape', ()))}")
+            # (all of it before the append: a call that is refused changes nothing)
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+            if t.device != self.cache.device:
+                raise ValueError(f"{name} must be on {self.cache.device}, is on {t.device}")
         if self.turns is not None or self.how["norm"] != "none":
             Q, K = zb_qk_norm_rope(Q, K, pos, self.turns, **self.how)
         K, V, Q = (t.reshape(-1, n, HEAD_DIM).contiguous() for t in (K, V, Q))

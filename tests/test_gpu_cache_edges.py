@@ -332,3 +332,21 @@ def test_layer_with_full_heads():
     assert not one.step(*split(X[:, :, :10])).any() and torch.equal(one.lens, lens)
     with pytest.raises(zb.ZbError, match="INDEX"):
         sync_ok()
+
+
+def test_layer_refuses_before_it_changes_anything():
+    import linear_hybrid_attention_b200 as zb
+    layer = zb.CachedAttention(1, 4, 2, 128)
+    X = _rand((1, 8, 3, 64), 122, 0.3)
+    Q, K, V = X[:, :4], X[:, 4:6], X[:, 6:]
+    layer.step(Q, K, V)
+    state = [t.clone() for t in (layer.lens, layer.cache.k, layer.cache.k_tail)]
+    for bad, err in (((Q.float(), K, V), TypeError), ((Q, K.float(), V), TypeError), ((Q, K, V.float()), TypeError),
+                     ((Q.cpu(), K, V), ValueError), ((Q, K, V.cpu()), ValueError)):
+        with pytest.raises(err):
+            layer.step(*bad)
+        assert all(torch.equal(a, b) for a, b in zip(state, (layer.lens, layer.cache.k, layer.cache.k_tail)))
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ValueError, match="scale"):
+            zb.CachedAttention(1, 4, 2, 128, scale=scale)
+    sync_ok()
