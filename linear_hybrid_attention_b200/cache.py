@@ -18,6 +18,8 @@ from .positions import RopeFrequencies, zb_qk_norm_rope
 __all__ = ["KV8Cache", "zb_kv8_append", "zb_kv8_read", "zb_kv8_attn", "zb_kv8_attn_workspace_bytes", "zb_kv8_evict",
            "CachedAttention"]
 
+# what a step's attention may take of workspace before it attends band by band (bytes)
+WORKSPACE_BOUND = 1 << 30
 FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
 
@@ -131,6 +133,14 @@ def zb_kv8_attn_workspace_bytes(cache: KV8Cache, heads_q: int, n_q: int, add_mas
     return int(_lib_handle().zb_kv8_attn_workspace_bytes(cache.struct, heads_q, n_q, 1 if add_mass else 0))
 
 
+def _ws_bytes(cache: KV8Cache, heads_q: int, n_q: int, add_mass: bool) -> int:
+    key = (heads_q, n_q, add_mass)
+    need = cache._ws_bytes.get(key)
+    if need is None:
+        need = cache._ws_bytes[key] = zb_kv8_attn_workspace_bytes(cache, heads_q, n_q, add_mass)
+    return need
+
+
 def zb_kv8_attn(Q, cache: KV8Cache, lens, causal: bool = False, scale: Optional[float] = None,
                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = False,
                 add_mass: bool = False, ws: Optional[torch.Tensor] = None):
@@ -147,11 +157,7 @@ def zb_kv8_attn(Q, cache: KV8Cache, lens, causal: bool = False, scale: Optional[
     if want_lse or lse is not None:
         lse = torch.empty_strided((heads_q, n_q), (n_q, 1), dtype=torch.float32, device=cache.device) if lse is None \
             else _out((heads_q, n_q), torch.float32, Q.device, lse, "lse")
-    key = (heads_q, n_q, add_mass)
-    need = cache._ws_bytes.get(key)
-    if need is None:
-        need = cache._ws_bytes[key] = zb_kv8_attn_workspace_bytes(cache, heads_q, n_q, add_mass)
-    ws = _ws(need, cache.device, ws)
+    ws = _ws(_ws_bytes(cache, heads_q, n_q, add_mass), cache.device, ws)
     for t, name in ((O, "O"), (lse, "lse"), (ws, "ws")):
         if t is not None and t.device != cache.device:
             raise ValueError(f"{name} must be on {cache.device}, is on {t.device}")
@@ -198,7 +204,8 @@ class CachedAttention:
     ``step(Q, K, V, pos)`` takes the new tokens' queries, keys and values ([B, heads, n, 64], any strides
     for Q and K), normalises and rotates Q and K, appends K and V, and returns the queries' attention over
     everything cached (``causal`` by default).  With ``budget`` (blocks a head) each step that attends adds
-    its softmax weight to the blocks', and ``evict()`` keeps the heaviest.  The lengths live on the device
+    its softmax weight to the blocks', and ``evict()`` keeps the heaviest; its workspace (one fp32 a query
+    row and 64 tokens of capacity) is held to 1 GiB by attending in bands of queries.  The lengths live on the device
     (``lens``, int32 [B * kv_heads]) and no call waits for the GPU, so a step can be captured in a graph and
     replayed.  Not for use from two streams at once: a step changes the cache.
     """
@@ -246,9 +253,26 @@ class CachedAttention:
         K, V, Q = (t.reshape(-1, n, HEAD_DIM).contiguous() for t in (K, V, Q))
         room = self.lens <= self.cache.capacity - n
         zb_kv8_append(self.cache, K, V, self.lens, lens_out=self.lens)
-        O = zb_kv8_attn(Q, self.cache, self.lens * room, causal=causal, scale=self.scale,
-                        add_mass=self.budget is not None)
+        how = dict(causal=causal, scale=self.scale, add_mass=self.budget is not None)
+        lens, band = self.lens * room, self._band(n)
+        if band >= n:
+            O = zb_kv8_attn(Q, self.cache, lens, **how)
+        else:
+            O = torch.empty_like(Q)
+            for end in range(band, n + band, band):
+                first, end = end - band, min(end, n)
+                # a causal band's queries are the newest of the tokens before its end
+                seen = lens - (n - end) if causal else lens
+                O[:, first:end] = zb_kv8_attn(Q[:, first:end].contiguous(), self.cache, seen, **how)
         return O.view(B, H, n, HEAD_DIM)
+
+    def _band(self, n: int) -> int:
+        """How many of n queries attend at once: with a budget the workspace grows with queries times capacity."""
+        if self.budget is None:
+            return n
+        while n > 1 and _ws_bytes(self.cache, self.batch * self.heads, n, True) > WORKSPACE_BOUND:
+            n = -(-n // 2)
+        return n
 
     def evict(self) -> torch.Tensor:
         """Keep at most ``budget`` blocks a head; returns the kept logical blocks (int32 [heads, budget], then -1)."""

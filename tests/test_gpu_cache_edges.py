@@ -350,3 +350,35 @@ def test_layer_refuses_before_it_changes_anything():
         with pytest.raises(ValueError, match="scale"):
             zb.CachedAttention(1, 4, 2, 128, scale=scale)
     sync_ok()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_layer_attends_in_bands(causal, monkeypatch):
+    """A step whose workspace would pass the bound attends band by band; a full head among the others."""
+    import linear_hybrid_attention_b200 as zb
+    from linear_hybrid_attention_b200 import cache as mod
+    B, H, G, n = 1, 6, 2, 700
+    make = lambda: zb.CachedAttention(B, H, G, 1024, 64, "e4m3", norm="rms", budget=16)
+    whole, banded = make(), make()
+    X = _rand((B, H + 2 * G, n, 64), 131, 0.3)
+    parts = (X[:, :H], X[:, H:H + G], X[:, H + G:])
+    for layer in (whole, banded):
+        layer.step(*(p[:, :, :100].contiguous() for p in parts))
+        layer.lens[1] = 400                              # 400 + 700 > 1024
+    want = whole.step(*parts, causal=causal)
+    sizes = []
+
+    def attn(Q, cache, lens, **how):
+        sizes.append((Q.shape[1], zb.zb_kv8_attn_workspace_bytes(cache, Q.shape[0], Q.shape[1], how["add_mass"])))
+        return zb.zb_kv8_attn(Q, cache, lens, **how)
+    bound = 83 << 18                                     # 350 queries need 20.76 MiB, 175 need 20.69
+    monkeypatch.setattr(mod, "WORKSPACE_BOUND", bound, raising=False)
+    monkeypatch.setattr(mod, "zb_kv8_attn", attn)
+    O = banded.step(*parts, causal=causal)
+    with pytest.raises(zb.ZbError, match="INDEX"):
+        sync_ok()
+    assert len(sizes) > 1 and sum(s for s, _ in sizes) == n and all(b <= bound for _, b in sizes), sizes
+    assert not O[:, 3:].any() and O[:, :3].any() and banded.lens.tolist() == [800, 400]
+    near = 2.0 ** -7 * want.float().abs() + 2.0 ** -9 * X.float().abs().max()
+    assert ((O.float() - want.float()).abs() <= near).all()
+    torch.testing.assert_close(banded.cache.mass, whole.cache.mass, rtol=2.0 ** -12, atol=1e-6)
