@@ -604,7 +604,7 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  * those tokens, query i to tokens 0 .. lens[h] - n_q + i (causal != 0).  A query
  * that sees no token gets zeros and an lse of -inf.
  *   in : Q bf16 [heads_q][n_q][64], heads_q a multiple of cache.heads;  lens
- *   out: O bf16 [heads_q][n_q][64];  lse fp32 [heads_q][n_q] natural-log
+ *   out: O bf16 [heads_q][n_q][64], not Q's memory;  lse fp32 [heads_q][n_q] natural-log
  *        log-sum-exp of each row's logits (may be NULL);  with add_mass, each
  *        block's softmax weight, summed over its tokens and the rows of its
  *        head's queries, is added to cache.mass (must not be NULL)
@@ -620,7 +620,7 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  * bits of their weights, and below 2^-40 (2^-31) may count as zeros; and a workspace
  * with add_mass holds one fp32 of every 64 tokens (every block, where smaller) of
  * the slots and row.
- * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0), ZB_ERR_NULL,
+ * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0, O == Q), ZB_ERR_NULL,
  * ZB_ERR_ALIGN, ZB_ERR_UNSUPPORTED (also more than 2^31 - 1 query rows of a cache
  * head), ZB_ERR_WORKSPACE, ZB_ERR_CUDA; ZB_ERR_TIMEOUT in the device status if a
  * bounded wait gave up.

@@ -870,6 +870,7 @@ extern "C" zb_status zb_kv8_attn(const uint16_t* Q, int32_t heads_q, int64_t n_q
     if (p.tiles * cache.heads > (1ll << 30) || p.tiles * cache.heads > (1ll << 37) / tiles) return ZB_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < p.total) return ZB_ERR_WORKSPACE;
     if (!aligned16(ws)) return ZB_ERR_ALIGN;
+    if (O == Q) return ZB_ERR_SHAPE;                 // a row's output is written while others' parts read its queries
     DeviceInfo dev;
     if ((e = current_device(&dev)) != ZB_OK) return e;
     if (dev.sm_count > kv8::MAX_SMS) return ZB_ERR_DEVICE;

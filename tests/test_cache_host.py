@@ -127,6 +127,11 @@ def test_attn_refusals(lib):
     assert at(ws=None) == 5 and at(wsb=need - 1) == 5
 
 
+def test_attn_refuses_its_queries_as_output(lib):
+    at = lambda n: lib.zb_kv8_attn(FAKE, 4, n, _cache(), FAKE, 0, 0.125, FAKE, None, 0, FAKE, 1 << 40, None)
+    assert at(1) == 2 and at(300) == 2
+
+
 def test_evict_refusals(lib):
     ev = lambda table=FAKE, mass=FAKE, lens=FAKE, H=2, S=9, B=64, budget=4, sinks=1, recent=2, out=FAKE + 64, lo=FAKE, \
         kept=None: lib.zb_kv8_evict(table, mass, lens, H, S, B, budget, sinks, recent, out, lo, kept, None)
