@@ -650,7 +650,7 @@ ZB_DEVINL void add_runs(const AttnArgs& a, int2 it, int r, int q, bool outputs, 
         for (int i = 0; i < n; ++i) {
             L += __shfl_sync(half, l, i, 16);
             const float fi = __shfl_sync(half, f, i, 16);
-            if (read && fi != 0.f) {
+            if (read) {                              // (a part without weight too: its values may be NaN)
                 const float4 w = v[static_cast<long long>(i) * TR * (HD / 4)];
                 s.x = fmaf(w.x, fi, s.x);
                 s.y = fmaf(w.y, fi, s.y);

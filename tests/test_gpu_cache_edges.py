@@ -234,6 +234,25 @@ def test_queries_that_are_not_finite_spoil_their_own_rows(block, G, n_q, causal)
     sync_ok()
 
 
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("rows", [1, 16, 33, 300])
+def test_values_that_are_nan_under_hardly_any_weight(block, rows):
+    # the weight underflows and the part that holds it is one of many: the outputs are NaN all the same
+    import linear_hybrid_attention_b200 as zb
+    n, q, scale = 40000, 4.0, 0.125
+    K = _rand((1, n, 64), 141, 0.3).float().cpu()
+    K[..., 0] = 0.0
+    K[:, 30000, 0] = 250.0 / (q * scale)
+    V = _rand((1, n, 64), 142).float().cpu()
+    V[0, 5, 9] = float("nan")
+    c, _, lens = _made(zb, K, V, block, "int8", 143)
+    Q = _rand((1, rows, 64), 144, 0.3)
+    Q[..., 0] = q
+    O, lse = zb.zb_kv8_attn(Q, c, lens, scale=scale, want_lse=True)
+    sync_ok()
+    assert torch.isnan(O).all() and torch.isfinite(lse).all()
+
+
 # --------------------------------------------------------------- exact rounding ----
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("low,high", [(1.0, 2.0), (2.0 ** -104, 2.0 ** -98), (2.0 ** -122, 2.0 ** -104), (2.0 ** -131, 2.0 ** -122)])
