@@ -499,7 +499,8 @@ typedef struct zb_qk_norm {
  * Queries and keys of a layer made ready for its attention in one pass:
  * y = w * (x - m) / sqrt(mean((x - m)^2) + eps) + b with m = 0 (ZB_NORM_RMS) or
  * the row's mean (ZB_NORM_LAYER), then the rotation; fp32 arithmetic, rounded to
- * bf16 once.  ZB_NORM_NONE ignores w and b and only rotates; rotary_dim 0 only
+ * bf16 once.  Rows may be of any size (their sums and products with w within
+ * fp32).  ZB_NORM_NONE ignores w and b and only rotates; rotary_dim 0 only
  * normalises.
  *   in : Q bf16, heads_q heads at q_rows; K bf16, heads_k heads at k_rows
  *        (heads_k 0: no keys, K and Ko are not looked at), e.g. both inside the

@@ -157,7 +157,21 @@ ZB_DEVINL float centre(f2* v, float eps) {
         q0 = f2_fma(v[i], v[i], q0);
         q1 = f2_fma(v[i + 1], v[i + 1], q1);
     }
-    return rsqrtf(row_sum(total(f2_add(q0, q1))) * (1.f / HD) + eps);
+    const float ms = row_sum(total(f2_add(q0, q1))) * (1.f / HD) + eps;
+    float inv = rsqrtf(ms);
+    // squares that pass fp32, or are lost below it: of the row times a power of two
+    if (__any_sync(0xffffffffu, !(ms >= 0x1p-90f && ms <= 0x1p100f))) {
+        const float s = ms > 1.f ? 0x1p-72f : 0x1p64f;
+        f2 q = 0ull;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const f2 x = f2_mul(v[i], f2_pack(s, s));
+            q = f2_fma(x, x, q);
+        }
+        const float far = rsqrtf(fmaf(row_sum(total(q)), 1.f / HD, eps * s * s)) * s;
+        if (!(ms >= 0x1p-90f && ms <= 0x1p100f)) inv = far;
+    }
+    return inv;
 }
 
 // sin and cos of a fraction of a turn (turns * 2^32).  After the exact reduction

@@ -340,3 +340,38 @@ def test_offsets_past_32_bits():
     assert torch.equal(view, d[0])
     assert zb.zb_rope(view, pos, turns, out=view) is view and torch.equal(view, zb.zb_rope(d[0], pos, turns))
     sync_ok()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_norm_of_rows_of_every_size(kind, eps):
+    """Rows whose squares pass fp32, or are lost below it, between ordinary ones.  Forward as above: a normalised row
+    is at most 8.  Backward, T the largest |w dy| of a row: dx = r (t - xh mean(t xh) - mean t) is at most 10 r T
+    before its last rounding, and fp32 arithmetic and the sines take 2^-17 of that."""
+    import linear_hybrid_attention_b200 as zb
+    N = 150
+    Q = _rand((1, 2, N, 64), 71)
+    size = torch.tensor([2.0 ** e for e in (-100, 118, 0, 70, -60, 55, -45)]).repeat(N)[:N]
+    Q = (Q.float() * size.cuda()[:, None]).bfloat16()
+    g = torch.Generator().manual_seed(72)
+    w, b = 1 + 0.3 * torch.randn(64, generator=g), 0.2 * torch.randn(64, generator=g) if kind == "layer" else None
+    pos = _pos(1, 1, N, 1000, 73)
+    fr, turns = _freq(zb, 64, 1, "none")
+    got, _ = zb.zb_qk_norm_rope(Q, None, pos.cuda(), turns, norm=kind, wq=w.cuda(), bq=None if b is None else b.cuda(), eps=eps)
+    sync_ok()
+    w64, b64 = w.double().numpy(), None if b is None else b.double().numpy()
+    e32 = float(np.float32(eps))
+    ref = oracle.qk_norm_rope(host(Q), w64, b64, kind, e32, pos.numpy(), fr.radians.numpy())
+    plain = oracle.qk_norm_rope(host(Q), w64, b64, kind, e32, None, None)
+    _close(got, ref, np.abs(plain).max(-1, keepdims=True) + np.abs(w64).max() * 1.0)
+    dy = _rand((1, 2, N, 64), 74, 0.3)
+    dQ, _, dwq, _, dbq, _ = zb.zb_qk_norm_rope_backward(dy, None, Q, None, pos.cuda(), turns, norm=kind, wq=w.cuda(), eps=eps)
+    sync_ok()
+    dx, dw, db = oracle.qk_norm_rope_grad(host(dy), host(Q), w64, kind, e32, pos.numpy(), fr.radians.numpy())
+    r = oracle.qk_norm(host(Q), kind, e32)[1]
+    T = np.abs(oracle.rope(host(dy), pos.numpy(), fr.radians.numpy(), inverse=True) * w64).max(-1, keepdims=True)
+    assert np.all(np.abs(host(dQ) - dx) <= HALF_BF16 * np.abs(dx) + 2.0 ** -17 * 10 * r * T)
+    # sums of 300 products of at most 8 |dy| each, whose errors are 2^-18 of that
+    assert np.all(np.abs(dwq.double().cpu().numpy() - dw) <= 300 * 2.0 ** -17 * 8 * np.abs(host(dy)).max())
+    if kind == "layer":
+        assert np.all(np.abs(dbq.double().cpu().numpy() - db) <= 300 * 2.0 ** -17 * np.abs(host(dy)).max())
