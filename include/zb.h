@@ -433,7 +433,8 @@ zb_status zb_gather_rows(const uint16_t* X, int32_t heads, int64_t n_in, int64_t
  *
  * zb_rope_frequencies writes, on the HOST, the frequencies as turns a position
  * in 64-bit fixed point (turns[i] = f_i / 2 pi * 2^64; what zb_rotation wants
- * on the device), so that angles of far positions lose nothing:
+ * on the device; computed in fp64, so good to some 2^-56 turns a position), so
+ * that angles of far positions are as good as those of near ones to that:
  *   ZB_ROPE_PLAIN   f_i = base^(-i / n)
  *   ZB_ROPE_LINEAR  f_i / factor
  *   ZB_ROPE_NTK     base * factor^(n / (n - 1)) in the place of base
@@ -554,7 +555,8 @@ zb_status zb_qk_norm_rope_backward(const uint16_t* dQo, const uint16_t* dKo, con
  *   mass             fp32 [heads][slots] or NULL: attention weight each slot's
  *                    block has received
  * The lengths are a separate DEVICE array int32 [heads].  A length out of
- * [0, slots * block] is cut to it; a table entry out of range is read as slot 0
+ * [0, slots * block] is cut to it (but zb_kv8_append takes no tokens there and
+ * leaves it as it is); a table entry out of range is read as slot 0
  * and sets ZB_ERR_INDEX in the device status.
  */
 enum { ZB_KV8_INT8 = 0, ZB_KV8_E4M3 = 1 };
@@ -617,8 +619,8 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  * of that (2^-31 and 2^-20 with more than 32 query rows of a cache head); sums, lse
  * and mass take it unrounded, and do not depend on the values.  The result does not
  * depend on scheduling.  With more than 32 query rows of a cache head, blocks whose
- * value scale is below 2^-24 (int8; e4m3: 2^-15) of the largest of their head lose
- * bits of their weights, and below 2^-40 (2^-31) may count as zeros; and a workspace
+ * value scale is below 2^-24 (int8; e4m3: 2^-15) of the largest of their head, or of
+ * 2^-96, lose bits of their weights, and below 2^-40 (2^-31) may count as zeros; and a workspace
  * with add_mass holds one fp32 of every 64 tokens (every block, where smaller) of
  * the slots and row.
  * Errors: ZB_ERR_SHAPE (also heads_q not a multiple, scale <= 0, O == Q), ZB_ERR_NULL,

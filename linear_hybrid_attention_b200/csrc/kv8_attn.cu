@@ -5,7 +5,8 @@
 //   O_r = sum_j p_rj s_v[block of j] code_j,     weight of block b = sum of p over
 //   its keys and the head's rows.
 //
-// Bound by the cache's bytes (128 a token): every byte is read once.  Work is cut
+// Bound by the cache's bytes (128 a token): every byte is read once, with 17 to 32 rows a
+// head twice (an item has at most 16).  Work is cut
 // into chunks of 64 keys, laid end to end over all heads (and 16-row tiles of
 // their queries); each warp takes an equal run of chunks, whatever the heads'
 // lengths, the 12 warps of a CTA neighbouring ones.  Lengths are read on the
@@ -37,7 +38,7 @@ namespace kv8 {
 
 // Twelve warps of two stages, not eight of three: the ring holds as much (192 KB),
 // and three warps a scheduler hide what two leave open (256 views, one token:
-// 145 -> 130 us).
+// 145 -> 130 us then; 117 with what came after).
 constexpr int WARPS = 12;
 constexpr int STAGES = 2;
 constexpr int TILE = 16;                         // most query rows of an item (8 if there are no more)
@@ -619,7 +620,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnArgs a) {
 // with a.groups, turns the rows' group sums into the blocks' weight.  Grid: (heads,
 // parts): every part works out the rows' log-sum-exp again, part 0 writes the
 // outputs, and the blocks are shared out over the parts.
-constexpr int FEW_ROWS = 32;                     // most rows a head that this kernel takes; kv8_tile.cu takes more
+// Most rows a head that this kernel takes; kv8_tile.cu takes more.  This kernel / that one
+// (us a call, int8 in blocks of 64): 16 heads of 43,968 tokens 74 / 67 at 33 to 48 rows
+// and 96 / 67 at 64; 16 of 1,024 20 / 17 and 22 / 17; 64 of 1,024 23 / 24 and 28 / 25; but
+// 256 of 300 26 / 40 and 33 / 41, 1,024 of 300 59 / 114 and 71 / 115: with many heads of a
+// few hundred tokens each 128-row tile costs more than the second reading of the cache.  The
+// lengths are on the device, so the rule does not follow them.
+constexpr int FEW_ROWS = 32;
 constexpr int JOIN_ROWS = FEW_ROWS;
 
 // One row's runs added up, by the 16 threads (one half warp) that hold 4 of its

@@ -30,9 +30,10 @@
 // of x, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 475 us without weights, 521 TFLOP/s (533 us causal with weights and both
-// joins); 1,280 rows 400 us, 576 TFLOP/s; e4m3 in blocks of 16, 1,374 rows 500 us.  Of
-// that the powers of two in the values cost 3 to 6% without weights, nothing with them.  A pair of 128 x 128 tiles takes about
+// tokens: 464 us without weights, 533 TFLOP/s (525 us causal with weights and both
+// joins); 1,280 rows 391 us, 589 TFLOP/s; 64 rows 70 us.  e4m3 in blocks of 16: 519 us,
+// 754, 436 and 77.  Keeping the values' powers of two apart from the weights costs 1 to 10% of
+// that without weights, nothing with them.  A pair of 128 x 128 tiles takes about
 // 3,500 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
 // pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P, and
 // waits of some 150 cycles each even where the phase is there: answering them by one
@@ -75,7 +76,7 @@ constexpr int K_MAX = FMT == ZB_KV8_INT8 ? 5 : 7;
 template <int FMT>
 constexpr int K_MIN = FMT == ZB_KV8_INT8 ? -24 : -15;
 constexpr int K_REST = 16;
-constexpr int NO_REF = -126;      // of a part without values yet: the smallest exponent of a scale
+constexpr int NO_REF = -96;       // the smallest reference, and that of a part without values yet
 ZB_DEVINL uint32_t ref_word(int ref) { return static_cast<uint32_t>(ref + 256) << 8; }
 ZB_DEVINL int word_ref(uint32_t word) { return static_cast<int>(word >> 8) - 256; }
 
@@ -85,7 +86,7 @@ struct __align__(1024) TileSmem {
     uint8_t v16[V16][TILE_BYTES];
     uint8_t raw[RAW][2][RAW_BYTES];
     float4 other[HD / 4][BM];         // slot 1's sums where it shares slot 0's rows
-    float2 other_ml[BM];
+    float4 other_ml[BM];              // maximum, sum, what the sums are to be multiplied by
     float4 sc[SC][8];                 // s_k, log2 f, 1 / f of 64 or 16 keys
     uint32_t v_mul[SC][8];            // the power of two of their values, a pair of fp16
     uint32_t sc_word[SC];             // bit g: s_v of group g is not finite; above: the reference of the values
@@ -426,16 +427,6 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
             Ring<SC> sc;
             bool ok = true;
             for (int part = 0; running; running = items.next(walk), ++part) {
-                if (walk.c0 == 0 && lane == 0) {
-                    // where the join finds the partial results of an item that begins in this run: this CTA's
-                    // place and how many CTAs hold parts, 0 for an item held whole.  The part's first tile and
-                    // the item's last one, in units of all items:
-                    const long long first = end - walk.left - (walk.c1 - walk.c0);
-                    const long long to = ((first + walk.nc) * ctas - 1) / total;
-                    a.item[items.index(walk)] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
-                                                          walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
-                }
-                if (!ok) continue;                             // the join reads all items all the same
                 int ref = NO_REF;
                 auto fetch = [&](int t, float& ks, float& vs) {
                     const long long key = static_cast<long long>(t) * BN + lane * KEYS;   // (t + lane / G, group lane % G)
@@ -446,8 +437,8 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                         vs = __ldg(c.v_scale + blk);
                     }
                 };
-                float ks, vs, ks_next = 0.f, vs_next = 0.f;
-                fetch(walk.c0, ks, vs);
+                float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+                if (ok) fetch(walk.c0, ks, vs);
                 for (int t0 = walk.c0; t0 < walk.c1 && ok; t0 += AHEAD) {
                     if (t0 + AHEAD < walk.c1) fetch(t0 + AHEAD, ks_next, vs_next);
                     const bool bad = !(fabsf(vs) <= 3.4e38f), some = !bad && vs > 0.f;
@@ -455,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     if (some) vs = fminf(vs, 0x1p122f);        // no block of bf16 values has more; 2^e stays a number
                     const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 126;   // subnormal: -126
                     const float frac = vs * pow2(-e);
-                    int top = some ? e : NO_REF;               // of the lane's tile
+                    int top = some ? max(e, NO_REF) : NO_REF;  // of the lane's tile
 #pragma unroll
                     for (int o = 1; o < G; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const int n = min(AHEAD, walk.c1 - t0);
@@ -481,6 +472,16 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     }
                     ks = ks_next;
                     vs = vs_next;
+                }
+                // (behind the scales, which others wait for; and after a wait that gave up too: the join reads it)
+                if (walk.c0 == 0 && lane == 0) {
+                    // where the join finds the partial results of an item that begins in this run: this CTA's
+                    // place and how many CTAs hold parts, 0 for an item held whole.  The part's first tile and
+                    // the item's last one, in units of all items:
+                    const long long first = end - walk.left - (walk.c1 - walk.c0);
+                    const long long to = ((first + walk.nc) * ctas - 1) / total;
+                    a.item[items.index(walk)] = make_int2(blockIdx.x * 2 + (part > 0 ? 1 : 0),
+                                                          walk.c1 == walk.nc ? 0 : static_cast<int>(to - blockIdx.x + 1));
                 }
             }
         }
@@ -756,31 +757,30 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < HD; ++e) o[e] = 0.f;
             }
-            {
-                // the row's outputs as they are, without the references: no part's depend on another's
-                const float inv = l == 0.f ? 0.f : 1.f / l;    // no key: zeros; NaN stays
-                const float size = pow2(word_ref(last));
+            // o times this and the share of the softmax sum: the outputs
+            const float size = nan_value ? __uint_as_float(0x7FC00000u) : pow2(word_ref(last));
+            if (PAIR) {
+                const float f = l == 0.f ? 0.f * size : size / l;  // no key: zeros; NaN stays
 #pragma unroll
-                for (int e = 0; e < HD; ++e) o[e] = nan_value ? __uint_as_float(0x7FC00000u) : o[e] * inv * size;
-            }
-            if (!PAIR) {
-                // the slots hold the same rows: slot 1 hands its outputs to slot 0
+                for (int e = 0; e < HD; ++e) o[e] *= f;
+            } else {
+                // the slots hold the same rows: slot 1 hands its sums to slot 0
                 if (s == 1) {
                     if (!(ok = wait_warp(smem_addr(&sm.other_empty), (part & 1) ^ 1, wc))) break;
 #pragma unroll
                     for (int i = 0; i < HD / 4; ++i)
                         sm.other[i][row] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    sm.other_ml[row] = make_float2(m, l);
+                    sm.other_ml[row] = make_float4(m, l, size, 0.f);
                     mbar_arrive(smem_addr(&sm.other_full));
                     continue;
                 }
                 if (!(ok = wait_warp(smem_addr(&sm.other_full), part & 1, wc))) break;
-                const float2 ml = sm.other_ml[row];
+                const float4 ml = sm.other_ml[row];
                 const float M = fmaxf(m, ml.x);
-                const float l0 = m == -INFINITY ? l : l * ex2(m - M), l1 = ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - M);
+                const float w0 = m == -INFINITY ? 1.f : ex2(m - M), w1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
                 m = M;
-                l = l0 + l1;
-                const float inv = l == 0.f ? 0.f : 1.f / l, f0 = l0 * inv, f1 = l1 * inv;
+                l = l * w0 + ml.y * w1;
+                const float inv = l == 0.f ? 0.f : 1.f / l, f0 = w0 * inv * size, f1 = w1 * inv * ml.z;
 #pragma unroll
                 for (int i = 0; i < HD / 4; ++i) {
                     const float4 w = sm.other[i][row];
@@ -840,28 +840,35 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const AttnArgs a) {
         const long long place = i == 0 ? it.x : (it.x / 2 + i) * 2;
         return (place * per_item + s) * BM + r;
     };
-    float M = -INFINITY, L = 0.f;
-    for (int i = q; i < it.y; i += 16) M = fmaxf(M, a.part_ml[at(i)].x);
+    auto part = [&](int i, int k) {
+        return i + k < it.y ? reinterpret_cast<const float4*>(a.part_o + at(i + k) * HD)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    // most rows have few parts: all loads of the first ones are under way before any is needed
+    const float2 ml = q < it.y ? a.part_ml[at(q)] : make_float2(-INFINITY, 0.f);
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = part(0, k);
+    float M = ml.x;
+    for (int i = q + 16; i < it.y; i += 16) M = fmaxf(M, a.part_ml[at(i)].x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
-    auto share = [&](int i) {                        // of the softmax sum, over 2^M
-        const float2 ml = a.part_ml[at(i)];
-        return ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - M);
-    };
-    for (int i = q; i < it.y; i += 16) L += share(i);
+    // a part's share of the softmax sum, over 2^M
+    auto share = [&](float2 p) { return p.y == 0.f ? 0.f : p.y * ex2(p.x - M); };
+    const float first = share(ml);
+    float L = first;
+    for (int i = q + 16; i < it.y; i += 16) L += share(a.part_ml[at(i)]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) L += __shfl_xor_sync(half, L, o);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < it.y; i0 += 16) {
-        const float f = i0 + q < it.y ? share(i0 + q) * inv : 0.f;
+        const float f = (i0 == 0 ? first : i0 + q < it.y ? share(a.part_ml[at(i0 + q)]) : 0.f) * inv;
         const int n = min(16, it.y - i0);
         for (int i1 = 0; i1 < n; i1 += 4) {
-            float4 v[4];
+            if (i0 + i1 > 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = i1 + k < n ? reinterpret_cast<const float4*>(a.part_o + at(i0 + i1 + k) * HD)[q]
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < 4; ++k) v[k] = part(i0 + i1, k);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {            // lanes past the last part hold zeros
                 const float fk = __shfl_sync(half, f, (i1 + k) & 15, 16);

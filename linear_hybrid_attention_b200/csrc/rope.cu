@@ -11,8 +11,8 @@
 //
 // Angles.  The frequency of pair i is held as turns a position in 64-bit fixed
 // point, T_i = f_i / 2 pi * 2^64; the low 64 bits of pos * T_i are then the
-// fraction of a turn, exact for any 32-bit position up to the rounding of T_i
-// (2^-65 turns a position).  Its top 32 bits go to sin and cos, so a far position
+// fraction of a turn, exact for any 32-bit position up to what T_i is off by: T_i comes
+// from fp64 (53 bits), some 2^-56 turns a position.  Its top 32 bits go to sin and cos, so a far position
 // costs no more and loses nothing against a near one.
 //
 // Both directions are HBM streams (a row in, a row out; backward two in, one
