@@ -617,8 +617,8 @@ zb_status zb_kv8_read(zb_kv8 cache, const int32_t* lens, int64_t n, uint16_t* K,
  * rounded to bf16 once.  A softmax weight enters the products as fp16: rounded to
  * 2^-11 of itself, and by up to 2^-39 of the row's largest where it is below 2^-28
  * of that (2^-31 and 2^-20 with more than 32 query rows of a cache head); sums, lse
- * and mass take it unrounded, and do not depend on the values.  The result does not
- * depend on scheduling.  With more than 32 query rows of a cache head, blocks whose
+ * and mass take it unrounded, and do not depend on the values.  Values below 2^-100
+ * may lose bits.  The result does not depend on scheduling.  With more than 32 query rows of a cache head, blocks whose
  * value scale is below 2^-24 (int8; e4m3: 2^-15) of the largest of their head, or of
  * 2^-96, lose bits of their weights, and below 2^-40 (2^-31) may count as zeros; and a workspace
  * with add_mass holds one fp32 of every 64 tokens (every block, where smaller) of

@@ -443,10 +443,9 @@ __global__ void __launch_bounds__(THREADS, 1) tile_kernel(const AttnArgs a) {
                     if (t0 + AHEAD < walk.c1) fetch(t0 + AHEAD, ks_next, vs_next);
                     const bool bad = !(fabsf(vs) <= 3.4e38f), some = !bad && vs > 0.f;
                     const uint32_t nan = __ballot_sync(0xffffffffu, bad);
-                    if (some) vs = fminf(vs, 0x1p122f);        // no block of bf16 values has more; 2^e stays a number
                     const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 126;   // subnormal: -126
-                    const float frac = vs * pow2(-e);
-                    int top = some ? max(e, NO_REF) : NO_REF;  // of the lane's tile
+                    const float frac = e > 2 ? vs * 0.25f * pow2(2 - e) : vs * pow2(-e);
+                    int top = some ? min(max(e, NO_REF), 127) : NO_REF;   // of the lane's tile; 2^top is a number
 #pragma unroll
                     for (int o = 1; o < G; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const int n = min(AHEAD, walk.c1 - t0);

@@ -152,6 +152,32 @@ def test_values_at_both_ends_of_their_type(G, n_q, causal):
     _check(zb, c, ora, lens, _rand((G, n_q, 64), 58, 0.3), G, causal, 0.125)
 
 
+@pytest.mark.parametrize("rows", [1, 40, 150])
+def test_scales_that_no_append_makes(rows):
+    # a cache filled by the caller: small codes under scales up to fp32's end, and zero codes under a scale of zero
+    import linear_hybrid_attention_b200 as zb
+    n, block = 320, 64
+    g = torch.Generator().manual_seed(59)
+    c, _, lens = _made(zb, _rand((1, n, 64), 59, 0.3).float(), torch.zeros((1, n, 64)), block, "int8", 60)
+    codes = torch.randint(-1, 2, (1, c.slots, block, 64), generator=g, dtype=torch.int8)
+    scales = torch.tensor([2.0 ** 126 * 1.75, 2.0 ** 127 * 1.5, 0.0, 2.0 ** 120, 3.0])
+    live = c.table[0, :5].long()
+    c.v.copy_(codes)
+    c.v_scale[0, live] = scales.cuda()
+    c.v[0, live[2]] = 0
+    V = (c.v[0, live].double().cpu() * scales.double()[:, None, None]).reshape(n, 64).numpy()
+    Q = _rand((1, rows, 64), 61, 0.3)
+    O = host(zb.zb_kv8_attn(Q, c, lens, scale=0.125))[0]
+    sync_ok()
+    k64 = c.k[0, live].double().cpu() * c.k_scale[0, live].double().cpu()[:, None, None]
+    k64, q64 = k64.reshape(n, 64).numpy(), host(Q)
+    ref = oracle.cache_attention(q64, k64, V, 0.125, False, block)[0][0]
+    absO = oracle.cache_attention(q64, k64, np.abs(V), 0.125, False, block)[0][0]
+    d = 64 * 2.0 ** -23 * 0.125 * np.max(np.abs(q64[0]) @ np.abs(k64).T, -1)[:, None]
+    bound = 2.0 ** -8 * np.abs(ref) + (2 * d + 2.0 ** -11 + 2.0 ** -18) * absO + 2.0 ** -31 * np.abs(V).sum(0)
+    assert np.all(np.abs(O - ref) <= bound), float(np.max(np.abs(O - ref) / bound))
+
+
 # ------------------------------------------------------------ logits, queries ----
 @pytest.mark.parametrize("block", [16, 64])
 @pytest.mark.parametrize("G,n_q,causal", ROWS)
