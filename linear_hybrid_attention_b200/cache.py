@@ -66,6 +66,8 @@ class KV8Cache:
             raise ValueError(f"format must be one of {sorted(FORMATS)}, got {format!r}")
         if heads < 1 or capacity < 1:
             raise ValueError(f"heads and capacity must be at least 1, got {heads} and {capacity}")
+        if block not in (16, 32, 64, 128):
+            raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
         slots = -(-capacity // block)
         z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
         codes = [z((heads, slots, block, HEAD_DIM), torch.uint8).view(FORMATS[format]) for _ in range(2)]
@@ -275,7 +277,9 @@ class CachedAttention:
         return n
 
     def evict(self) -> torch.Tensor:
-        """Keep at most ``budget`` blocks a head; returns the kept logical blocks (int32 [heads, budget], then -1)."""
+        """Keep at most ``budget`` blocks a head; returns the kept logical blocks (int32 [heads, budget], then -1).
+
+        The tensor is the layer's own, and the next call writes it again."""
         if self.budget is None:
             raise ValueError("evict() needs a layer made with a budget")
         c = self.cache

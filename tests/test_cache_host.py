@@ -154,3 +154,10 @@ def test_bindings_refuse_cpu_tensors():
         zb.CachedAttention(1, 5, 2, 100, device="cpu")
     with pytest.raises(ValueError, match="format"):
         zb.KV8Cache.empty(2, 100, format="int4", device="cpu")
+
+
+def test_empty_cache_refuses_blocks():
+    import linear_hybrid_attention_b200 as zb
+    for block in (0, -16, 48):
+        with pytest.raises(ValueError, match="block"):
+            zb.KV8Cache.empty(2, 100, block, device="cpu")
