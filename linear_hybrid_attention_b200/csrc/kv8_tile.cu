@@ -30,10 +30,10 @@
 // of x, raised only when it grows by more than RAISE.
 //
 // Measured at 16 heads x 1,374 rows (12 row tiles with the last) against 43,968 int8
-// tokens: 464 us without weights, 533 TFLOP/s (525 us causal with weights and both
-// joins); 1,280 rows 391 us, 589 TFLOP/s; 64 rows 70 us.  e4m3 in blocks of 16: 519 us,
-// 754, 436 and 77.  Keeping the values' powers of two apart from the weights costs 1 to 10% of
-// that without weights, nothing with them.  A pair of 128 x 128 tiles takes about
+// tokens: 465 us without weights, 532 TFLOP/s (510 us causal with weights and both
+// joins); 1,280 rows 391 us, 589 TFLOP/s; 64 rows 70 us.  e4m3 in blocks of 16: 528 us,
+// 756, 445 and 78.  Keeping the values' powers of two apart from the weights costs 2% of that
+// without weights (e4m3 in blocks of 16: 12%), nothing with them.  A pair of 128 x 128 tiles takes about
 // 3,500 cycles, 2,048 of them the MUFU's 256 exponentials a scheduler, the tensor
 // pipe's some 1,050; what is left is a warp's own chain (read S, maximum, write P, and
 // waits of some 150 cycles each even where the phase is there: answering them by one
